@@ -1,0 +1,166 @@
+// Block-scaled FP8 GEMM, device side: what its kernels share.
+//
+//   Y[m][n] = bf16( act( sum_k (sx qx)[m][k] (sw qw)[n][k] + bias[n] ) )
+//
+// The products run as tcgen05.mma kind::mxf8f6f4 with block scales: the tensor
+// core takes a ue8m0 byte per row and 32 elements from tensor memory and adds
+// sx sw qx qw into an fp32 accumulator.  A block of 128 elements is four MMAs
+// of K = 32 that all name the same byte: a scale word in tensor memory holds
+// the bytes of four consecutive blocks, and the instruction's scale-factor ids
+// pick one, so one 512-byte copy per 128 rows serves 512 elements along K.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "device_common.cuh"
+#include "fp8_layout.h"
+#include "svdq_internal.h"
+
+namespace svdq {
+namespace fp8 {
+
+struct Params {
+  const uint8_t *x;             // activation codes [KS][Mp][128]
+  const uint32_t *sx;           // activation scale words [KW][Mp]
+  const uint8_t *w;             // weight codes [experts][NT][KS][16 KB]
+  const uint8_t *sw;            // weight scale atoms [experts][NT][KW][512]
+  const uint16_t *bias;         // [experts][N] bf16 or null
+  uint16_t *Y;
+  size_t ldy;
+  const int *offsets;           // [experts + 1] or null: one expert with all rows
+  int experts, M, Mp, N, ntn, KS, KW, gelu_col_begin;
+  unsigned int *status;
+  unsigned long long limit_ns;
+};
+
+// D(tmem) (+)= sum over K of (A . 2^sfa) (B . 2^sfb)^T, e4m3 inputs, one ue8m0 scale per 32 elements.
+__device__ __forceinline__ void umma_mxf8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.block32 [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+          d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+      : "memory");
+}
+
+// Instruction descriptor: A and B e4m3 (0), ue8m0 scales (bit 23), N >> 3 at 17, M >> 4 at 24, K-major.
+__host__ __device__ constexpr uint32_t idesc_mxf8(int m, int n) {
+  return (1u << 23) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+// ... with byte `id` of both scale words (B's id at bit 4, A's at bit 29).
+__device__ __forceinline__ uint32_t with_scale_byte(uint32_t idesc, uint32_t id) {
+  return idesc | (id << 4) | (id << 29);
+}
+
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// GELU, tanh form, of two values: 0.5 y (1 + tanh z) = y / (1 + exp(-2 z)), z = sqrt(2/pi) (y + 0.044715 y^3):
+// no cancellation for negative y, and exp and the reciprocal come from the hardware approximations (a few
+// 1e-7 relative), far below the bf16 rounding of the result.  exp(-2 z) overflows to infinity only where the
+// result is below 1e-37, and 1 / infinity is the 0 it rounds to.
+__device__ __forceinline__ float2 gelu_tanh2(float2 y) {
+  const float2 y2 = dev::mul2_rn(y, y);
+  // -2 z log2(e) = y (c0 + c1 y^2), c0 = -2 sqrt(2/pi) log2(e), c1 = 0.044715 c0
+  const float2 p = dev::fma2_rn(make_float2(-0.10294324f, -0.10294324f), y2, make_float2(-2.3022082f, -2.3022082f));
+  const float2 z = dev::mul2_rn(y, p);
+  return make_float2(y.x * dev::rcp_approx_ftz(1.0f + dev::ex2_approx_ftz(z.x)),
+                     y.y * dev::rcp_approx_ftz(1.0f + dev::ex2_approx_ftz(z.y)));
+}
+template <int EPI>
+__device__ __forceinline__ float2 activate2(float2 y) {
+  if constexpr (EPI == SVDQ_EPILOGUE_GELU_ERF) return dev::gelu_erf2(y);
+  if constexpr (EPI == SVDQ_EPILOGUE_GELU_TANH) return gelu_tanh2(y);
+  return y;
+}
+
+// Rows and token tiles of the experts, in shared memory: expert e owns rows
+// [start[e], start[e + 1]) and token tiles [tiles[e], tiles[e + 1]).  Offsets
+// are taken as they come and clamped: into [0, M], and never below an earlier
+// one, so whatever they hold, the experts' rows are disjoint and inside Y.
+// Token tiles start at a multiple of 8 rows (where operand rows may start),
+// at or before the expert's first row.
+struct ExpertTable {
+  int start[FP8_MAX_EXPERTS + 1];
+  int tiles[FP8_MAX_EXPERTS + 1];
+};
+
+// Fills the table; called by one full warp.
+__device__ __forceinline__ void fill_expert_table(const Params &p, int tile_rows, ExpertTable *t) {
+  const int lane = threadIdx.x & 31;
+  if (p.offsets == nullptr) {
+    if (lane == 0) {
+      t->start[0] = 0;
+      t->start[1] = p.M;
+      t->tiles[0] = 0;
+      t->tiles[1] = (p.M + tile_rows - 1) / tile_rows;
+    }
+    return;
+  }
+  int first = min(max(__ldcg(p.offsets), 0), p.M);   // start of the expert `base`, the same in every lane
+  int tiles = 0;
+  for (int base = 0; base < p.experts; base += 32) {
+    const int e = base + lane;
+    int end = e < p.experts ? min(max(__ldcg(p.offsets + e + 1), 0), p.M) : 0;
+    end = max(end, first);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {               // running maximum of the ends
+      const int v = __shfl_up_sync(0xFFFFFFFFu, end, o);
+      if (lane >= o) end = max(end, v);
+    }
+    int start = __shfl_up_sync(0xFFFFFFFFu, end, 1);
+    if (lane == 0) start = first;
+    const int mine = e < p.experts && end > start ? (end - (start & ~7) + tile_rows - 1) / tile_rows : 0;
+    int sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    if (e < p.experts) {
+      t->start[e] = start;
+      t->tiles[e] = tiles + sum - mine;
+      if (e == p.experts - 1) {
+        t->start[p.experts] = end;
+        t->tiles[p.experts] = tiles + sum;
+      }
+    }
+    first = __shfl_sync(0xFFFFFFFFu, end, 31);
+    tiles += __shfl_sync(0xFFFFFFFFu, sum, 31);
+  }
+}
+
+// A unit of work: the token tile [row0, row0 + tile_rows) of an expert against weight tile nt.  Rows below
+// `begin` or from `end` on belong to others.  An expert's units are consecutive, its token tiles fastest:
+// the units that share a weight tile run at the same time and read it from DRAM once.
+struct Item {
+  int expert, nt, row0, begin, end;
+};
+__device__ __forceinline__ Item find_item(const Params &p, const ExpertTable *t, int tile_rows, int nt_count, int item) {
+  int lo = 0, hi = p.experts;                         // the last expert whose first unit is <= item
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (t->tiles[mid] * nt_count <= item) lo = mid;
+    else hi = mid;
+  }
+  const int mts = t->tiles[lo + 1] - t->tiles[lo];
+  const int r = item - t->tiles[lo] * nt_count;
+  Item it;
+  it.expert = lo;
+  it.nt = r / mts;
+  it.begin = t->start[lo];
+  it.end = t->start[lo + 1];
+  it.row0 = (it.begin & ~7) + (r % mts) * tile_rows;
+  return it;
+}
+
+}  // namespace fp8
+}  // namespace svdq

@@ -1,11 +1,18 @@
 """User-facing layers on top of the C ABI: SVDQLinear (W4A4 + low-rank branch),
-SVDQLinearInt4 (its INT4 variant) and AWQLinear (W4A16).  They hold the packed weights on the GPU and reuse
-activation buffers per row count; all arithmetic runs in the library.
+SVDQLinearInt4 (its INT4 variant), AWQLinear (W4A16), FP8Linear and FP8Experts (block-scaled FP8, dense and by
+expert), and RotaryND (rotary positions over several axes).  They hold the packed weights on the GPU; all
+arithmetic runs in the library.
 
-A layer instance keeps one set of activation buffers per row count, shared by
-all its calls: use an instance from one stream at a time (two calls with the
-same row count that overlap on different streams would race on them).
+The 4-bit layers keep one set of activation buffers per row count, shared by
+all their calls: use such an instance from one stream at a time (two calls
+with the same row count that overlap on different streams would race on them).
+FP8Linear, FP8Experts and RotaryND keep nothing from one call for the next:
+their workspaces and outputs come from torch's allocator, on the stream the
+call runs on, so an instance may be used from several streams and captured
+into several graphs.
 """
+import ctypes
+
 import numpy as np
 import torch
 
@@ -323,3 +330,164 @@ class AWQLinear:
             lib.awq_linear_w4a16(X, self.inv_awq, self.qweight, self.scales, self.zeros, self.bias, self.N, Y,
                                  stream=stream)
         return Y
+
+
+def _on(device, stream, call):
+    """call(raw stream) with `device` current and torch allocating on the stream the work runs on: `stream`, else
+    the caller's current stream of that device."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the layer on {device}")
+        with torch.cuda.stream(stream):       # makes the stream's device current as well
+            return call(stream.cuda_stream)
+    if torch.cuda.current_device() == device.index:
+        return call(_raw_stream(None, device))
+    with torch.cuda.device(device):
+        return call(_raw_stream(None, device))
+
+
+class FP8Linear:
+    """Y = epilogue(q(X) q(W) + b) in block-scaled FP8: e4m3 codes under one power-of-two scale per 128 elements
+    along K, for every row of X and every column of W (for projections that 4 bits lose too much of).
+
+    weight: bf16 CUDA [K, N], quantized once here; bias: bf16 CUDA [N] or None.  `from_weight` takes the host
+    arrays the other layers take.
+    """
+
+    experts = None
+
+    def __init__(self, weight, bias=None, epilogue=lib.EPILOGUE_NONE, gelu_col_begin=0):
+        name = type(self).__name__
+        lead = () if self.experts is None else (self.experts,)
+        if weight.dim() != len(lead) + 2 or weight.dtype != torch.bfloat16 or not weight.is_cuda:
+            raise ValueError(f"{name}: weight must be a bf16 CUDA tensor {'[experts, K, N]' if lead else '[K, N]'}, "
+                             f"got {weight.dtype} {tuple(weight.shape)} on {weight.device}")
+        self.K, self.N = weight.shape[-2:]
+        if epilogue not in (lib.EPILOGUE_NONE, lib.EPILOGUE_GELU_ERF, lib.EPILOGUE_GELU_TANH):
+            raise ValueError(f"{name}: unknown epilogue {epilogue}")
+        if not 0 <= gelu_col_begin <= self.N:
+            raise ValueError(f"{name}: gelu_col_begin must be in [0, {self.N}]")
+        self.epilogue, self.gelu_col_begin = epilogue, gelu_col_begin
+        self.device = _resolve(weight.device)
+        if bias is not None and (tuple(bias.shape) != (*lead, self.N) or bias.dtype != torch.bfloat16
+                                 or bias.device != self.device):
+            raise ValueError(f"{name}: bias must be bf16 {[*lead, self.N]} on {self.device}")
+        _init_on(self.device)
+        self.bias = bias.contiguous() if bias is not None else None
+        with torch.cuda.device(self.device):
+            self.packed = lib.fp8_pack_weights(weight if weight.stride(-1) == 1 else weight.contiguous())
+            torch.cuda.current_stream().synchronize()   # ready on every stream from here on
+
+    @classmethod
+    def from_weight(cls, W_bits, bias_bits=None, epilogue=lib.EPILOGUE_NONE, gelu_col_begin=0, device="cuda"):
+        """From uint16 arrays of bf16 patterns on the host."""
+        device = _resolve(device)
+        bias = None if bias_bits is None else _dev(bias_bits, device, torch.bfloat16)
+        return cls(_dev(W_bits, device, torch.bfloat16), bias, epilogue, gelu_col_begin)
+
+    def _run(self, X, offsets, Y, stream):
+        name = type(self).__name__
+        _check_input(X, self.K, self.device, name)
+        M = X.shape[0]
+        if X.stride(1) != 1:
+            raise ValueError(f"{name}: X must have unit stride in its last dimension")
+        if Y is not None:
+            _check_output(Y, M, self.N, self.device, name)
+            if Y.stride(1) != 1:
+                raise ValueError(f"{name}: Y must have unit stride in its last dimension")
+
+        def call(s):
+            out = Y if Y is not None else torch.empty((M, self.N), dtype=torch.bfloat16, device=self.device)
+            ws = torch.empty(lib.fp8_workspace_size(M, self.K), dtype=torch.uint8, device=self.device)
+            ldx, ldy = (X.stride(0), out.stride(0)) if M > 1 else (self.K, self.N)
+            bias = None if self.bias is None else self.bias.data_ptr()
+            L = lib.load()
+            if offsets is None:
+                lib._check("fp8_linear", L.fp8_linear(
+                    X.data_ptr(), M, self.K, ldx, self.packed.data_ptr(), bias, self.N, self.epilogue,
+                    self.gelu_col_begin, out.data_ptr(), ldy, ws.data_ptr(), s))
+            else:
+                lib._check("fp8_linear_grouped", L.fp8_linear_grouped(
+                    X.data_ptr(), M, self.K, ldx, offsets.data_ptr(), self.experts, self.packed.data_ptr(), bias,
+                    self.N, self.epilogue, self.gelu_col_begin, out.data_ptr(), ldy, ws.data_ptr(), s))
+            return out
+
+        return _on(self.device, stream, call)
+
+    def __call__(self, X, Y=None, stream=None):
+        """X: bf16 CUDA [M, K] -> bf16 [M, N] (into Y if given)."""
+        return self._run(X, None, Y, stream)
+
+
+class FP8Experts(FP8Linear):
+    """The FP8 product by expert: rows offsets[e] .. offsets[e+1]-1 of X meet weight e, any share of the rows.
+
+    weight: bf16 CUDA [experts, K, N]; bias: bf16 CUDA [experts, N] or None.  `offsets` stay on the device (int32
+    [experts + 1], not decreasing); rows of Y outside every expert's are left as they were (zeros when the call
+    allocates Y).
+    """
+
+    def __init__(self, weight, bias=None, epilogue=lib.EPILOGUE_NONE, gelu_col_begin=0):
+        self.experts = weight.shape[0] if weight.dim() == 3 else 0
+        super().__init__(weight, bias, epilogue, gelu_col_begin)
+
+    def __call__(self, X, offsets, Y=None, stream=None):
+        if (offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() != self.experts + 1
+                or offsets.device != self.device or not offsets.is_contiguous()):
+            raise ValueError(f"FP8Experts: offsets must be contiguous int32 [{self.experts + 1}] on {self.device}, got "
+                             f"{offsets.dtype} {tuple(offsets.shape)} on {offsets.device}")
+        if Y is None:
+            Y = _on(self.device, stream, lambda s: torch.zeros((X.shape[0], self.N), dtype=torch.bfloat16,
+                                                               device=self.device))
+        return self._run(X, offsets, Y, stream)
+
+
+class RotaryND:
+    """Rotary positions over several axes for query and key heads, after an optional RMS norm of each head.
+
+    axis_dims: the share of the head dimension each axis turns (even, adding up to D); pair j of an axis of d
+    dimensions turns by position * theta^(-2j/d).  interleaved: pairs are neighbours (2i, 2i+1), else i and
+    i + D/2.  q_norm, k_norm: bf16 CUDA [D] norm weights or None.
+    """
+
+    def __init__(self, axis_dims, theta=10000.0, interleaved=True, q_norm=None, k_norm=None, eps=1e-6, device="cuda"):
+        axis_dims = [int(d) for d in axis_dims]
+        D = sum(axis_dims)
+        if not axis_dims or any(d < 2 or d % 2 for d in axis_dims) or D % 8 or D > 256:
+            raise ValueError(f"RotaryND: axis_dims {axis_dims} must be even and add up to a multiple of 8, at most 256")
+        if not theta > 0:
+            raise ValueError("RotaryND: theta must be positive")
+        self.D, self.axes, self.eps = D, len(axis_dims), float(eps)
+        self.device = _resolve(device)
+        for w in (q_norm, k_norm):
+            if w is not None and (w.dtype != torch.bfloat16 or w.numel() != D or w.device != self.device):
+                raise ValueError(f"RotaryND: a norm weight must be bf16 [{D}] on {self.device}")
+        _init_on(self.device)
+        self.q_norm = None if q_norm is None else q_norm.contiguous()
+        self.k_norm = None if k_norm is None else k_norm.contiguous()
+        pairs = [(a, float(theta) ** (-2.0 * j / d)) for a, d in enumerate(axis_dims) for j in range(d // 2)]
+        self.plan = lib.RopePlan(D, self.axes, lib.ROPE_ND_INTERLEAVED if interleaved else lib.ROPE_ND_HALF)
+        for i, (a, f) in enumerate(pairs):
+            self.plan.axis[i], self.plan.freq[i] = a, f
+
+    def __call__(self, q, k, pos, q_out=None, k_out=None, inverse=False, stream=None):
+        """q: bf16 CUDA [M, heads, D] (any row and head strides), k likewise or None; pos: int32 or float32
+        [M, axes].  Returns (q_out, k_out); q_out may be q, k_out may be k.  inverse: turns back."""
+        if q.dim() != 3 or pos.dim() != 2 or pos.shape[0] != q.shape[0]:
+            raise ValueError(f"RotaryND: q must be [M, heads, {self.D}] and pos [M, {self.axes}], got "
+                             f"{tuple(q.shape)} and {tuple(pos.shape)}")
+        if k is None and k_out is not None:
+            raise ValueError("RotaryND: k_out without k")
+        for t in (q, k, pos, q_out, k_out):
+            if t is not None and t.device != self.device:
+                raise ValueError(f"RotaryND: every tensor must be on {self.device}, got {t.device}")
+
+        def call(s):
+            qo = q_out if q_out is not None else torch.empty(q.shape, dtype=torch.bfloat16, device=self.device)
+            ko = k_out if k_out is not None or k is None else torch.empty(k.shape, dtype=torch.bfloat16,
+                                                                          device=self.device)
+            lib.rope_nd(q, k, self.plan, pos, qo, ko, self.q_norm, self.k_norm if k is not None else None, inverse,
+                        self.eps, ctypes.c_void_p(s))
+            return qo, ko
+
+        return _on(self.device, stream, call)

@@ -58,6 +58,24 @@ class AwqProblem(ctypes.Structure):
 
 
 AWQ_MAX_GROUP = 128
+FP8_BLOCK = 128
+FP8_MAX_EXPERTS = 512
+ROPE_ND_INTERLEAVED = 0
+ROPE_ND_HALF = 1
+
+
+class RopePlan(ctypes.Structure):
+    """rope_nd_plan of include/svdq.h."""
+    _fields_ = [("D", ctypes.c_int), ("axes", ctypes.c_int), ("pairing", ctypes.c_int),
+                ("axis", ctypes.c_ubyte * 128), ("freq", ctypes.c_double * 128)]
+
+
+class RopeTensor(ctypes.Structure):
+    """rope_nd_tensor of include/svdq.h."""
+    _fields_ = [("X", ctypes.c_void_p), ("x_row", ctypes.c_int64), ("x_head", ctypes.c_int64), ("Y", ctypes.c_void_p),
+                ("y_row", ctypes.c_int64), ("y_head", ctypes.c_int64), ("norm", ctypes.c_void_p),
+                ("heads", ctypes.c_int)]
+
 
 _SIGNATURES = {
     "svdq_version": (_I, []),
@@ -94,6 +112,14 @@ _SIGNATURES = {
     "awq_linear_w4a16_gemm": (_I, [_P, _I, _I, _I, _P, _P, _P, _P, _I, _P, _I, _P, _I, _P, _P]),
     "awq_expand_weights": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _P]),
     "awq_linear_w4a16_expanded": (_I, [_P, _I, _I, _I, _P, _I, _P, _I, _P, _P]),
+    "fp8_weight_size": (_I, [_I, _I, _I, _SZ]),
+    "fp8_workspace_size": (_I, [_I, _I, _SZ]),
+    "fp8_pack_weights": (_I, [_P, _I, _I, _I, ctypes.c_int64, _I, _P, _P]),
+    "fp8_quantize_act": (_I, [_P, _I, _I, _I, _P, _P]),
+    "fp8_linear": (_I, [_P, _I, _I, _I, _P, _P, _I, _I, _I, _P, _I, _P, _P]),
+    "fp8_linear_grouped": (_I, [_P, _I, _I, _I, _P, _I, _P, _P, _I, _I, _I, _P, _I, _P, _P]),
+    "rope_nd": (_I, [ctypes.POINTER(RopeTensor), ctypes.POINTER(RopeTensor), _I, ctypes.POINTER(RopePlan), _P,
+                     ctypes.c_int64, _I, _I, ctypes.c_float, _P]),
     "svdq_check_status": (_I, [_P]),
     "svdq_debug_wait_timeout": (_I, [ctypes.c_uint64, _P]),
     "svdq_debug_convert": (_I, [_P, _I, _P, _P, _P]),
@@ -150,6 +176,13 @@ def _dptr(t, name, dtype=None, allow_none=False):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _dptr_any(t, name):
+    """Device pointer of a CUDA tensor of any type and strides."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return ctypes.c_void_p(t.data_ptr())
+
+
 def _nbytes(t):
     return t.numel() * t.element_size()
 
@@ -168,6 +201,8 @@ def _need_2d(t, rows, cols, name):
 
 def _stream(stream):
     import torch
+    if isinstance(stream, ctypes.c_void_p):     # a raw handle
+        return stream
     s = stream if stream is not None else torch.cuda.current_stream()
     return ctypes.c_void_p(s.cuda_stream)
 
@@ -665,6 +700,126 @@ def awq_linear_w4a16_expanded(X, bias, N, Y, workspace, M=None, K=None, stream=N
     _check("awq_linear_w4a16_expanded", load().awq_linear_w4a16_expanded(
         _dptr(X, "X", torch.bfloat16), M, K, X.stride(0), _dptr(bias, "bias", allow_none=True), N,
         _dptr(Y, "Y", torch.bfloat16), Y.stride(0), _dptr(workspace, "workspace"), _stream(stream)))
+
+
+@functools.lru_cache(maxsize=1024)
+def fp8_weight_size(K, N, experts=1):
+    """Bytes of a packed FP8 weight (the library's answer, cached per shape)."""
+    n = ctypes.c_size_t()
+    _check("fp8_weight_size", load().fp8_weight_size(K, N, experts, ctypes.byref(n)))
+    return n.value
+
+
+@functools.lru_cache(maxsize=1024)
+def fp8_workspace_size(M, K):
+    """Bytes of the workspace of an FP8 call with M rows (cached per shape)."""
+    n = ctypes.c_size_t()
+    _check("fp8_workspace_size", load().fp8_workspace_size(M, K, ctypes.byref(n)))
+    return n.value
+
+
+def _row_stride(t, cols):
+    """Row stride of a 2-D tensor; a single row's is its width, whatever torch recorded for it."""
+    return t.stride(0) if t.shape[0] != 1 else cols
+
+
+def fp8_pack_weights(W, packed=None, stream=None):
+    """Quantizes bf16 CUDA weights W [K, N], or [experts, K, N], into a packed weight (u8 CUDA, allocated if
+    not given)."""
+    import torch
+    if W.dim() not in (2, 3):
+        raise ValueError(f"W must be [K, N] or [experts, K, N], got {tuple(W.shape)}")
+    E, K, N = (1, *W.shape) if W.dim() == 2 else W.shape
+    need = fp8_weight_size(K, N, E)
+    p = _dptr(W, "W", torch.bfloat16)
+    if packed is None:
+        packed = torch.empty(need, dtype=torch.uint8, device=W.device)
+    _need_bytes(packed, need, "packed")
+    _check("fp8_pack_weights", load().fp8_pack_weights(
+        p, K, N, W.stride(-2), W.stride(0) if E > 1 else 0, E, _dptr(packed, "packed", torch.uint8), _stream(stream)))
+    return packed
+
+
+def fp8_quantize_act(X, workspace, stream=None):
+    """Enqueues the FP8 activation quantizer.  X: bf16 CUDA [M, K] (row stride ldx)."""
+    import torch
+    M, K = X.shape
+    _need_bytes(workspace, fp8_workspace_size(M, K), "workspace")
+    _check("fp8_quantize_act", load().fp8_quantize_act(
+        _dptr(X, "X", torch.bfloat16), M, K, _row_stride(X, K), _dptr(workspace, "workspace", torch.uint8),
+        _stream(stream)))
+
+
+def fp8_linear(X, packed, bias, N, epilogue, gelu_col_begin, Y, workspace, stream=None):
+    """Enqueues the FP8 linear layer.  X: bf16 CUDA [M, K]; Y: bf16 CUDA [M, N] (row strides ldx, ldy)."""
+    import torch
+    M, K = X.shape
+    _need_bytes(packed, fp8_weight_size(K, N), "packed")
+    _need_bytes(workspace, fp8_workspace_size(M, K), "workspace")
+    _need_bytes(bias, 2 * N, "bias")
+    _need_2d(Y, M, N, "Y")
+    _check("fp8_linear", load().fp8_linear(
+        _dptr(X, "X", torch.bfloat16), M, K, _row_stride(X, K), _dptr(packed, "packed", torch.uint8),
+        _dptr(bias, "bias", torch.bfloat16, allow_none=True), N, epilogue, gelu_col_begin,
+        _dptr(Y, "Y", torch.bfloat16), _row_stride(Y, N), _dptr(workspace, "workspace", torch.uint8),
+        _stream(stream)))
+
+
+def fp8_linear_grouped(X, offsets, packed, bias, N, epilogue, gelu_col_begin, Y, workspace, stream=None):
+    """Enqueues the FP8 product by expert.  X: bf16 CUDA [M, K]; offsets: int32 CUDA [experts + 1]; bias: bf16
+    CUDA [experts, N] or None; Y: bf16 CUDA [M, N]."""
+    import torch
+    M, K = X.shape
+    E = offsets.numel() - 1
+    _need_bytes(packed, fp8_weight_size(K, N, E), "packed")
+    _need_bytes(workspace, fp8_workspace_size(M, K), "workspace")
+    _need_bytes(bias, 2 * N * E, "bias")
+    _need_2d(Y, M, N, "Y")
+    if offsets.dim() != 1 or not offsets.is_contiguous() or (bias is not None and not bias.is_contiguous()):
+        raise ValueError("offsets and bias must be contiguous, offsets 1-D")
+    _check("fp8_linear_grouped", load().fp8_linear_grouped(
+        _dptr(X, "X", torch.bfloat16), M, K, _row_stride(X, K), _dptr(offsets, "offsets", torch.int32), E,
+        _dptr(packed, "packed", torch.uint8), _dptr(bias, "bias", torch.bfloat16, allow_none=True), N, epilogue,
+        gelu_col_begin, _dptr(Y, "Y", torch.bfloat16), _row_stride(Y, N),
+        _dptr(workspace, "workspace", torch.uint8), _stream(stream)))
+
+
+def _rope_tensor(x, y, norm, M, D, name):
+    """Checks one tensor's heads [M, heads, D] and returns its RopeTensor."""
+    import torch
+    if x.dim() != 3 or x.shape[0] != M or x.shape[2] != D or tuple(y.shape) != tuple(x.shape):
+        raise ValueError(f"{name} must be [{M}, heads, {D}] and its output alike, got {tuple(x.shape)} and "
+                         f"{tuple(y.shape)}")
+    if x.dtype is not torch.bfloat16 or y.dtype is not torch.bfloat16:
+        raise ValueError(f"{name} must have dtype {torch.bfloat16}, got {x.dtype} and {y.dtype}")
+    if not (x.is_cuda and y.is_cuda):
+        raise ValueError(f"{name} must be a CUDA tensor")
+    H = x.shape[1]
+    xs, ys = x.stride(), y.stride()
+    if xs[2] != 1 or ys[2] != 1:
+        raise ValueError(f"{name} must have unit stride in its last dimension")
+    return RopeTensor(x.data_ptr(), xs[0] if M > 1 else 0, xs[1] if H > 1 else 0, y.data_ptr(), ys[0] if M > 1 else 0,
+                      ys[1] if H > 1 else 0, None if norm is None else norm.data_ptr(), H)
+
+
+def rope_nd(q, k, plan, pos, q_out, k_out, q_norm=None, k_norm=None, inverse=False, eps=1e-6, stream=None):
+    """Enqueues the rotary positions of q [M, heads, D] and k (likewise, or None), bf16 CUDA, into q_out and
+    k_out (which may be q and k).  pos: int32 or float32 CUDA [M, axes]; norms: bf16 CUDA [D] or None."""
+    import torch
+    M, D = pos.shape[0], plan.D
+    if pos.dim() != 2 or pos.shape[1] != plan.axes or (plan.axes > 1 and pos.stride(1) != 1):
+        raise ValueError(f"pos must be [M, {plan.axes}] with unit stride in its last dimension, got {tuple(pos.shape)}")
+    if pos.dtype not in (torch.int32, torch.float32):
+        raise ValueError(f"pos must be int32 or float32, got {pos.dtype}")
+    for norm in (q_norm, k_norm):
+        if norm is not None and (norm.dtype is not torch.bfloat16 or norm.numel() != D or not norm.is_contiguous()
+                                 or not norm.is_cuda):
+            raise ValueError(f"a norm weight must be bf16 CUDA [{D}]")
+    tq = _rope_tensor(q, q_out, q_norm, M, D, "q")
+    tk = None if k is None else ctypes.byref(_rope_tensor(k, k_out, k_norm, M, D, "k"))
+    _check("rope_nd", load().rope_nd(
+        ctypes.byref(tq), tk, M, ctypes.byref(plan), _dptr_any(pos, "pos"), pos.stride(0) if M > 1 else 0,
+        pos.dtype is torch.float32, bool(inverse), eps, _stream(stream)))
 
 
 def svdq_check_status(stream=None):

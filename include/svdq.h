@@ -537,6 +537,118 @@ int svdq_linear_int4(const uint8_t *a_codes, const void *a_scales, const void *U
                      const void *w_scales, const void *l2t, const void *bias, int M, int N, int K, int rank,
                      int epilogue, int gelu_col_begin, void *Y, int ldy, svdq_stream_t stream);
 
+/* ------------------------------------------------------- block-scaled FP8
+ * The projections that a checkpoint keeps above 4 bits, in 8: e4m3 codes under
+ * one power-of-two scale per block of 128 elements along K, for every
+ * activation row and every output column of the weight:
+ *   amax = largest finite |x| of the block (0 if none)
+ *   s = 2^e, e the smallest integer >= -127 with amax <= 448 * 2^e
+ *   code = e4m3(x / s), round to nearest even (x / s is exact, nothing saturates)
+ * and, with q(x) = code * s,
+ *   Y[m][n] = bf16( epilogue( sum_k q(X[m][k]) q(W[k][n]) + bias[n] ) )
+ * with fp32 accumulation.  An infinity or a NaN becomes the NaN code (e4m3 has
+ * no infinity): the row (of X) or column (of W) that holds it gives NaN.
+ */
+#define FP8_MAX_EXPERTS 512
+
+/* Bytes of a packed weight: `experts` matrices of K x N (1 for fp8_linear).
+ * Rules: K >= 8, K % 8 == 0, N >= 8, N % 8 == 0, 1 <= experts <= FP8_MAX_EXPERTS. */
+int fp8_weight_size(int K, int N, int experts, size_t *bytes);
+
+/* Bytes of the workspace of a call with M rows: the quantized activations.
+ * Rules: M >= 1, K >= 8, K % 8 == 0. */
+int fp8_workspace_size(int M, int K, size_t *bytes);
+
+/*
+ * Quantizes bf16 weights on the GPU into `packed` (fp8_weight_size bytes, an
+ * opaque layout: swizzled tiles of 128 output columns x 128 k, then the scale
+ * words).  W: `experts` matrices [K][ldw] bf16, expert_stride elements apart
+ * (any alignment of a bf16 is enough here).
+ * Rules: those of fp8_weight_size, ldw >= N, expert_stride >= 0.
+ */
+int fp8_pack_weights(const void *W, int K, int N, int ldw, int64_t expert_stride, int experts, void *packed,
+                     svdq_stream_t stream);
+
+/*
+ * The activation quantizer of the two calls below, by itself.  workspace
+ * (fp8_workspace_size(M, K) bytes) receives, with KS = ceil(K/128),
+ * KW = ceil(KS/4) and Mp = M rounded up to 8: codes [KS][Mp][128] (16-byte
+ * chunk c of row m at chunk c ^ (m % 8); 0 past K), then the scale words
+ * [KW][Mp]: byte j of word (w, m) is e + 127 of block 4w + j.  Rows M..Mp-1 are
+ * not written.
+ * Rules: M >= 1, K >= 8, K % 8 == 0, ldx >= K, ldx % 8 == 0.
+ */
+int fp8_quantize_act(const void *X, int M, int K, int ldx, void *workspace, svdq_stream_t stream);
+
+/*
+ * The linear layer: quantizes X [M][ldx] bf16 into workspace and multiplies.
+ * packed from fp8_pack_weights (experts = 1); bias [N] bf16 or NULL; the
+ * epilogue's GELU applies from column gelu_col_begin on; Y [M][ldy] bf16.
+ * workspace: fp8_workspace_size(M, K) bytes, in use until the call has run on
+ * the stream (calls that may overlap take workspaces of their own).
+ * Rules: those of fp8_quantize_act, N >= 8, N % 8 == 0, ldy >= N, ldy % 8 == 0,
+ * 0 <= gelu_col_begin <= N.
+ */
+int fp8_linear(const void *X, int M, int K, int ldx, const void *packed, const void *bias, int N, int epilogue,
+               int gelu_col_begin, void *Y, int ldy, void *workspace, svdq_stream_t stream);
+
+/*
+ * The product by expert: rows offsets[e] .. offsets[e+1]-1 of X meet expert e's
+ * weight and bias row, for e < experts; any share, none included.  offsets:
+ * DEVICE array of experts + 1 int32, not decreasing, read by the kernel (it may
+ * come from an earlier kernel of the stream).  Rows of Y outside every expert's
+ * are left as they were.  The host cannot judge offsets: they are clamped on
+ * the device into [0, M] and to the largest offset before them, so no value of
+ * theirs leads outside X or Y.
+ * packed: `experts` weights; bias [experts][N] bf16 or NULL.  The rest as
+ * fp8_linear.  Rules: those of fp8_linear, 1 <= experts <= FP8_MAX_EXPERTS.
+ */
+int fp8_linear_grouped(const void *X, int M, int K, int ldx, const int32_t *offsets, int experts, const void *packed,
+                       const void *bias, int N, int epilogue, int gelu_col_begin, void *Y, int ldy, void *workspace,
+                       svdq_stream_t stream);
+
+/* ------------------------------------------------------- rotary positions
+ * Rotary position embedding over several axes for the query and key heads of a
+ * projection's output, after an optional RMS norm of each head:
+ *   x = norm ? x * rsqrt(mean over the head of x^2 + eps) * norm : x
+ *   pair i of a head turned by angle pos[m][axis[i]] * freq[i] (float64):
+ *   (x, y) -> (x cos - y sin, x sin + y cos)
+ * in float32, rounded once to bf16.
+ */
+enum rope_nd_pairing {
+  ROPE_ND_INTERLEAVED = 0,        /* pair i: elements 2i and 2i + 1 of the head */
+  ROPE_ND_HALF = 1                /* pair i: elements i and i + D/2 */
+};
+/* What the pairs of a head turn by (a HOST structure, read during the call). */
+typedef struct rope_nd_plan {
+  int D;                          /* head dimension */
+  int axes;                       /* columns of pos */
+  int pairing;                    /* rope_nd_pairing */
+  unsigned char axis[128];        /* [D/2] axis of each pair */
+  double freq[128];               /* [D/2] radians per position of each pair */
+} rope_nd_plan_t;
+/* The heads of one tensor (HOST structure).  Strides in elements. */
+typedef struct rope_nd_tensor {
+  const void *X;                  /* bf16, element d of head h of row m at m x_row + h x_head + d */
+  int64_t x_row, x_head;
+  void *Y;                        /* bf16, likewise; may be X with the same strides */
+  int64_t y_row, y_head;
+  const void *norm;               /* [D] bf16 norm weight or NULL (no norm) */
+  int heads;
+} rope_nd_tensor_t;
+/*
+ * Turns the heads of Q and of K (NULL: none) by one set of positions.
+ * pos: M rows of `axes` values, pos_row elements apart: int32, or float32 with
+ * pos_is_float.  inverse: by the negated angle (undoes a turn; also the turn's
+ * gradient); not with a norm.
+ * Rules: M >= 1; 8 <= D <= 256, D % 8 == 0; 1 <= axes <= D/2; axis[i] < axes;
+ * 1 <= heads <= 65535; strides multiples of 8; pointers 16-byte aligned (pos
+ * 4-byte); pos_row >= 0 (0: one position for all rows); the heads of a Y must
+ * not overlap one another.
+ */
+int rope_nd(const rope_nd_tensor_t *Q, const rope_nd_tensor_t *K, int M, const rope_nd_plan_t *plan, const void *pos,
+            int64_t pos_row, int pos_is_float, int inverse, float eps, svdq_stream_t stream);
+
 /*
  * Self-test of the bounded wait used by every kernel: launches one block that
  * waits on a shared-memory barrier nothing will ever complete, with a limit

@@ -1,0 +1,110 @@
+"""Refusals and size queries of the block-scaled FP8 calls and of rope_nd, without a GPU: every check happens
+before anything touches the device."""
+import ctypes
+
+import pytest
+import torch
+
+from bit_w4a4_diffusion_smooth_b200 import layer, lib
+
+P = ctypes.c_void_p(16)        # never dereferenced
+ODD = ctypes.c_void_p(24)
+
+
+def test_sizes():
+    # K = 136: two stages, one scale word; N = 136: two weight tiles; 9 rows take 16
+    assert lib.fp8_weight_size(136, 136, 3) == 3 * 2 * (2 * 16384 + 512)
+    assert lib.fp8_workspace_size(9, 136) == 2 * 16 * 128 + 16 * 4
+    assert lib.fp8_workspace_size(1, 8) == 8 * 128 + 8 * 4
+    for bad in ((0, 8), (12, 8), (8, 0), (8, 12), (8, 8, 0), (8, 8, 513)):
+        with pytest.raises(lib.SvdqError) as e:
+            lib.fp8_weight_size(*bad)
+        assert e.value.status == lib.ERR_SHAPE
+    for bad in ((0, 8), (1, 4), (1, 0), (-1, 8)):
+        with pytest.raises(lib.SvdqError) as e:
+            lib.fp8_workspace_size(*bad)
+        assert e.value.status == lib.ERR_SHAPE
+
+
+def _linear(x=P, M=4, K=64, ldx=64, w=P, bias=None, N=64, epi=0, begin=0, y=P, ldy=64, ws=P):
+    return lib.load().fp8_linear(x, M, K, ldx, w, bias, N, epi, begin, y, ldy, ws, None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(x=None), lib.ERR_INVALID_ARG), (dict(w=None), lib.ERR_INVALID_ARG), (dict(y=None), lib.ERR_INVALID_ARG),
+    (dict(ws=None), lib.ERR_INVALID_ARG), (dict(epi=3), lib.ERR_INVALID_ARG), (dict(epi=-1), lib.ERR_INVALID_ARG),
+    (dict(M=0), lib.ERR_SHAPE), (dict(M=-5), lib.ERR_SHAPE), (dict(K=60), lib.ERR_SHAPE), (dict(K=0), lib.ERR_SHAPE),
+    (dict(N=60), lib.ERR_SHAPE), (dict(N=0), lib.ERR_SHAPE), (dict(ldx=56), lib.ERR_SHAPE), (dict(ldx=68), lib.ERR_SHAPE),
+    (dict(ldy=56), lib.ERR_SHAPE), (dict(ldy=68), lib.ERR_SHAPE), (dict(begin=-1), lib.ERR_SHAPE),
+    (dict(begin=65), lib.ERR_SHAPE), (dict(M=2 ** 31 - 1, N=2 ** 20, ldy=2 ** 20), lib.ERR_SHAPE),
+    (dict(x=ODD), lib.ERR_ALIGNMENT), (dict(w=ODD), lib.ERR_ALIGNMENT), (dict(y=ODD), lib.ERR_ALIGNMENT),
+    (dict(ws=ODD), lib.ERR_ALIGNMENT)])
+def test_fp8_linear_refuses(kw, want):
+    assert _linear(**kw) == want
+
+
+def test_fp8_grouped_pack_and_quantize_refuse():
+    so = lib.load()
+    g = lambda off=P, E=2, M=4: so.fp8_linear_grouped(P, M, 64, 64, off, E, P, None, 64, 0, 0, P, 64, P, None)
+    assert g(off=None) == lib.ERR_INVALID_ARG
+    assert g(E=0) == lib.ERR_SHAPE and g(E=513) == lib.ERR_SHAPE and g(M=0) == lib.ERR_SHAPE
+    k = lambda W=P, K=64, N=64, ldw=64, st=0, E=1, out=P: so.fp8_pack_weights(W, K, N, ldw, st, E, out, None)
+    assert k(W=None) == lib.ERR_INVALID_ARG and k(out=None) == lib.ERR_INVALID_ARG and k(out=ODD) == lib.ERR_ALIGNMENT
+    assert k(K=4) == lib.ERR_SHAPE and k(N=4) == lib.ERR_SHAPE and k(ldw=63) == lib.ERR_SHAPE
+    assert k(E=0) == lib.ERR_SHAPE and k(E=2, st=-1) == lib.ERR_SHAPE
+    q = lambda X=P, M=4, K=64, ldx=64, ws=P: so.fp8_quantize_act(X, M, K, ldx, ws, None)
+    assert q(X=None) == lib.ERR_INVALID_ARG and q(ws=None) == lib.ERR_INVALID_ARG
+    assert q(M=0) == lib.ERR_SHAPE and q(K=4) == lib.ERR_SHAPE and q(ldx=60) == lib.ERR_SHAPE
+    assert q(X=ODD) == lib.ERR_ALIGNMENT and q(ws=ODD) == lib.ERR_ALIGNMENT
+
+
+def _plan(D=16, axes=2, pairing=0):
+    p = lib.RopePlan(D, axes, pairing)
+    for i in range(min(D // 2, 128)):
+        p.axis[i], p.freq[i] = i % max(axes, 1), 1.0
+    return p
+
+
+def _rope(q=None, k=None, M=4, plan=None, pos=P, row=2, inverse=0):
+    mk = lambda t: None if t is None else ctypes.byref(lib.RopeTensor(*t))
+    q = (16, 32, 16, 32, 32, 16, None, 2) if q is None else q
+    plan = _plan() if plan is None else plan
+    return lib.load().rope_nd(mk(q), mk(k), M, ctypes.byref(plan), pos, row, 0, inverse, 1e-6, None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(pos=None), lib.ERR_INVALID_ARG), (dict(M=0), lib.ERR_SHAPE), (dict(row=-1), lib.ERR_SHAPE),
+    (dict(plan=_plan(pairing=2)), lib.ERR_INVALID_ARG), (dict(plan=_plan(D=12)), lib.ERR_SHAPE),
+    (dict(plan=_plan(D=264)), lib.ERR_SHAPE), (dict(plan=_plan(D=0)), lib.ERR_SHAPE), (dict(plan=_plan(axes=0)), lib.ERR_SHAPE),
+    (dict(plan=_plan(axes=9)), lib.ERR_SHAPE), (dict(pos=ctypes.c_void_p(18)), lib.ERR_ALIGNMENT),
+    # X, x_row, x_head, Y, y_row, y_head, norm, heads
+    (dict(q=(None, 32, 16, 32, 32, 16, None, 2)), lib.ERR_INVALID_ARG),
+    (dict(q=(16, 32, 16, None, 32, 16, None, 2)), lib.ERR_INVALID_ARG),
+    (dict(q=(24, 32, 16, 32, 32, 16, None, 2)), lib.ERR_ALIGNMENT),
+    (dict(q=(16, 36, 16, 32, 32, 16, None, 2)), lib.ERR_ALIGNMENT),
+    (dict(q=(16, 32, 16, 32, 32, 16, 24, 2)), lib.ERR_ALIGNMENT),
+    (dict(q=(16, 32, 16, 32, 32, 16, None, 0)), lib.ERR_SHAPE),
+    (dict(q=(16, 32, 16, 32, 24, 16, None, 2)), lib.ERR_SHAPE),      # rows of Y overlap
+    (dict(q=(16, 32, 16, 32, 32, 8, None, 2)), lib.ERR_SHAPE),       # heads of Y overlap
+    (dict(q=(16, 32, 16, 32, 16, 48, None, 2)), lib.ERR_SHAPE),      # head-major, 4 rows of 16 in 48
+    (dict(q=(16, 32, 16, 16, 64, 16, None, 2)), lib.ERR_INVALID_ARG),  # in place with other strides
+    (dict(q=(16, 32, 16, 32, 32, 16, 64, 2), inverse=1), lib.ERR_INVALID_ARG),
+    (dict(k=(16, 32, 16, 32, 32, 16, 64, 2), inverse=1), lib.ERR_INVALID_ARG),
+    (dict(k=(16, 32, 16, 24, 32, 16, None, 2)), lib.ERR_ALIGNMENT)])
+def test_rope_refuses(kw, want):
+    assert _rope(**kw) == want
+
+
+def test_rope_refuses_an_axis_that_pos_lacks():
+    p = _plan()
+    p.axis[3] = 2
+    assert _rope(plan=p) == lib.ERR_SHAPE
+
+
+def test_layers_refuse_host_tensors_and_bad_shapes():
+    w = torch.zeros(64, 64, dtype=torch.bfloat16)
+    for make in (lambda: layer.FP8Linear(w), lambda: layer.FP8Experts(w[None]), lambda: layer.FP8Linear(w[None]),
+                 lambda: layer.RotaryND([16, 3], device="cpu"), lambda: layer.RotaryND([]),
+                 lambda: layer.RotaryND([4]), lambda: layer.RotaryND([200, 64]), lambda: layer.RotaryND([16], theta=0)):
+        with pytest.raises(ValueError):
+            make()
