@@ -213,6 +213,14 @@ extern "C" int svdq_init(int device) {
     return fail(SVDQ_ERR_CUDA, std::string("cudaGetDeviceCount: ") + cudaGetErrorString(e));
   }
   if (device < 0 || device >= count) return fail(SVDQ_ERR_INVALID_ARG, "svdq_init: no such device");
+  {
+    // already validated: only make it current (reading the properties takes milliseconds)
+    std::lock_guard<std::mutex> lock(g_state_mutex);
+    if (device < static_cast<int>(g_states.size()) && g_states[device].initialized) {
+      e = cudaSetDevice(device);
+      return e == cudaSuccess ? ok() : fail(SVDQ_ERR_CUDA, std::string("cudaSetDevice: ") + cudaGetErrorString(e));
+    }
+  }
   cudaDeviceProp prop;
   e = cudaGetDeviceProperties(&prop, device);
   if (e != cudaSuccess) return fail(SVDQ_ERR_CUDA, std::string("cudaGetDeviceProperties: ") + cudaGetErrorString(e));

@@ -29,6 +29,7 @@ namespace fp8 {
 
 int launch_quantize_act(const char *fn, const void *X, int M, int K, int ldx, void *workspace, int sm_count,
                         cudaStream_t stream);
+int launch_gemm_pair(const char *fn, const Params &p, int epilogue, int sm_count, cudaStream_t stream);
 
 namespace {
 
@@ -349,6 +350,10 @@ int run(const char *fn, const void *X, int M, int K, int ldx, const int *offsets
   p.limit_ns = kWaitLimitNs;
   // rows per token tile: the smallest that holds an expert's average share
   const long long share = (static_cast<long long>(M) + experts - 1) / experts;
+  if (share > 128) {
+    rc = launch_gemm_pair(fn, p, epilogue, st->sm_count, stream);
+    return rc == SVDQ_OK ? ok() : rc;
+  }
   const int tok = share <= 16 ? 16 : share <= 32 ? 32 : share <= 64 ? 64 : 128;
   const long long units = (static_cast<long long>(M) / tok + (experts > 1 ? 2ll * experts : 1)) * p.ntn;
   rc = tok == 16   ? launch<16>(fn, p, epilogue, units, st->sm_count, stream)
