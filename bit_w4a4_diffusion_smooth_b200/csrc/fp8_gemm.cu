@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_gemm_kernel(const __grid_const
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
+    if (elect_one()) {
       int it = 0;
       bool ok = true;
       for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_gemm_kernel(const __grid_const
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ scales into TMEM, MMAs
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t idesc = idesc_mxf8(kTileN, TOK);
       int it = 0, quad = 0, n = 0;
       bool ok = true, issued = false;

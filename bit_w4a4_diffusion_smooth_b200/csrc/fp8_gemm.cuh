@@ -45,6 +45,16 @@ __device__ __forceinline__ void umma_mxf8(uint32_t d_tmem, uint64_t a_desc, uint
       : "memory");
 }
 
+// True in one lane of a full, converged warp.  Code under `if (elect_one())` is known to run in a single thread, so
+// the operands of tcgen05 and bulk-copy instructions go straight to uniform registers; under `if (lane == 0)` the
+// compiler has to allow for several and issues each through a loop: 200 cycles an MMA against 110, measured on
+// the 256 x 256 x 32 MMAs, which take 128.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t pred;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(pred));
+  return pred != 0;
+}
+
 // Instruction descriptor: A and B e4m3 (0), ue8m0 scales (bit 23), N >> 3 at 17, M >> 4 at 24, K-major.
 __host__ __device__ constexpr uint32_t idesc_mxf8(int m, int n) {
   return (1u << 23) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);

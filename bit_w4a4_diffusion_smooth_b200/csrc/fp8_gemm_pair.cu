@@ -10,12 +10,12 @@
 // Roles (one CTA per SM, persistent over units of work, 12 warps):
 //   warp 0      producer in both CTAs: per k-stage its 16 KB halves of the two
 //               operands, completing on the even CTA's `full` barrier
-//   warp 1      owns TMEM (pair allocation); in the even CTA one thread copies
-//               the scale words into both TMEMs (tcgen05.cp, every fourth
-//               stage), issues the MMAs and commits each stage to both CTAs
+//   warp 1      owns TMEM (pair allocation); in the even CTA one thread issues
+//               the MMAs and commits each stage to both CTAs
 //   warp 2      scale words of the next four stages, in both CTAs: the words
 //               of its own 128 token rows and of all 256 weight rows (which
 //               both TMEMs need)
+//   warp 3      even CTA: copies them into both TMEMs (tcgen05.cp)
 //   warps 4-11  epilogue in both CTAs: drain the accumulator into registers,
 //               hand TMEM back, then bias, GELU, bf16, and 32 x 32 tiles
 //               through shared memory, written by TMA where the tile lies
@@ -82,10 +82,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   uint64_t *empty = full + STAGES;                                  // both CTAs: stage free again
   uint64_t *sf_full = empty + STAGES;                               // even CTA: both CTAs' scale words
   uint64_t *sf_empty = sf_full + SF_BUFS;                           // both CTAs
-  uint64_t *tmem_full = sf_empty + SF_BUFS;                         // both CTAs: accumulator ready
+  uint64_t *sf_tmem = sf_empty + SF_BUFS;                           // even CTA: scale words in both TMEMs
+  uint64_t *tmem_full = sf_tmem + SF_BUFS;                         // both CTAs: accumulator ready
   uint64_t *tmem_empty = tmem_full + 1;                             // even CTA: both CTAs drained it
   uint64_t *drain = tmem_empty + 1;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+  uint64_t *drain_cp = drain + 1;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain_cp + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   ExpertTable *tab = reinterpret_cast<ExpertTable *>(smem + TAB_OFF);
 
@@ -104,10 +106,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     for (int b = 0; b < SF_BUFS; ++b) {
       dev::mbar_init(&sf_full[b], 2);
       dev::mbar_init(&sf_empty[b], 1);
+      dev::mbar_init(&sf_tmem[b], 1);
     }
     dev::mbar_init(tmem_full, 1);
     dev::mbar_init(tmem_empty, 2 * EPI_WARPS);
     dev::mbar_init(drain, 1);
+    dev::mbar_init(drain_cp, 1);
     *abort_flag = 0;
     dev::fence_mbar_init();
   }
@@ -127,7 +131,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer (both CTAs)
-    if (lane == 0) {
+    if (elect_one()) {
       dev::prefetch_tmap(&maps.x);
       dev::prefetch_tmap(&maps.w);
       int it = 0;
@@ -161,7 +165,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ scales into TMEM, MMAs (even CTA)
-    if (h == 0 && lane == 0) {
+    if (h == 0 && elect_one()) {
       constexpr uint32_t idesc = idesc_mxf8(256, 256);
       int it = 0, quad = 0, n = 0;
       bool ok = true, issued = false;
@@ -175,18 +179,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         for (int ks = 0; ks < p.KS; ++ks, ++it) {
           const int s = it % STAGES, b = quad % SF_BUFS;
           if ((ks & 3) == 0) {
-            if (!dev::mbar_wait_cluster(&sf_full[b], (quad / SF_BUFS) & 1, p.limit_ns, abort_flag)) {
+            if (!dev::mbar_wait(&sf_tmem[b], (quad / SF_BUFS) & 1, p.limit_ns, abort_flag)) {
               ok = false;
               break;
             }
-            dev::tc_fence_after();
-            const uint32_t src = dev::smem_u32(smem + SF_OFF + b * SF_BYTES);
             sfx = tmem + SF_COL + 12 * b;
             sfw = sfx + 4;
-            dev::tmem_cp_32x128b_x4_pair(sfx, dev::desc_sf(src));
-            dev::tmem_cp_32x128b_x4_pair(sfw, dev::desc_sf(src + kScaleAtom));
-            dev::tmem_cp_32x128b_x4_pair(sfw + 4, dev::desc_sf(src + 2 * kScaleAtom));
-            issued = true;
           }
           if (!dev::mbar_wait_cluster(&full[s], (it / STAGES) & 1, p.limit_ns, abort_flag)) {
             ok = false;
@@ -199,6 +197,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           for (int j = 0; j < 4; ++j)
             umma_mxf8_pair(tmem, dev::desc_sw128(sx + 32 * j), dev::desc_sw128(sw + 32 * j), id, sfx, sfw,
                            ks > 0 || j > 0 ? 1u : 0u);
+          issued = true;
           dev::tc_commit_pair_mc(&empty[s], 0x3);
           if ((ks & 3) == 3 || ks == p.KS - 1) {
             dev::tc_commit_pair_mc(&sf_empty[b], 0x3);
@@ -249,6 +248,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
     }
     if (!ok && lane == 0) abort_pair(abort_flag, peer_abort, p.status);
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ scale words into TMEM (even CTA)
+    // from a warp of its own: in the MMA thread's order the copies would stand between the MMAs
+    if (h == 0 && elect_one()) {
+      int quad = 0;
+      bool ok = true;
+      for (int item = pair; item < items && ok; item += pairs) {
+        for (int kw = 0; kw < p.KW; ++kw, ++quad) {
+          const int b = quad % SF_BUFS;
+          if (!dev::mbar_wait_cluster(&sf_full[b], (quad / SF_BUFS) & 1, p.limit_ns, abort_flag)) {
+            ok = false;
+            break;
+          }
+          dev::tc_fence_after();
+          const uint32_t src = dev::smem_u32(smem + SF_OFF + b * SF_BYTES);
+          const uint32_t dst = tmem + SF_COL + 12 * b;
+          dev::tmem_cp_32x128b_x4_pair(dst, dev::desc_sf(src));
+          dev::tmem_cp_32x128b_x4_pair(dst + 4, dev::desc_sf(src + kScaleAtom));
+          dev::tmem_cp_32x128b_x4_pair(dst + 8, dev::desc_sf(src + 2 * kScaleAtom));
+          dev::tc_commit_pair(&sf_tmem[b]);
+        }
+      }
+      if (!ok) abort_pair(abort_flag, peer_abort, p.status);
+      if (quad > 0) {
+        dev::tc_commit_pair(drain_cp);
+        dev::mbar_wait(drain_cp, 0, p.limit_ns, nullptr);
+      }
+    }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue (both CTAs)
     const int e = warp - 4, q = warp & 3, half = e >> 2;   // TMEM lane quarter; which 128 of the 256 columns
