@@ -20,15 +20,17 @@ namespace svdq {
 namespace fp8 {
 
 struct Params {
-  const uint8_t *x;             // activation codes [KS][Mp][128]
-  const uint32_t *sx;           // activation scale words [KW][Mp]
-  const uint8_t *w;             // weight codes [experts][NT][KS][16 KB]
-  const uint8_t *sw;            // weight scale atoms [experts][NT][KW][512]
+  const uint16_t *X;            // activations [M][ldx] bf16
+  size_t ldx;
+  const uint8_t *x;             // their codes [KS][Mp][128] and
+  const uint32_t *sx;           // scale words [KW][Mp] (many rows only)
+  const uint8_t *w;             // weight codes [experts][KS][N][128]
+  const uint32_t *sw;           // weight scale words [experts][KW][N]
   const uint16_t *bias;         // [experts][N] bf16 or null
   uint16_t *Y;
   size_t ldy;
   const int *offsets;           // [experts + 1] or null: one expert with all rows
-  int experts, M, Mp, N, ntn, KS, KW, gelu_col_begin;
+  int experts, M, Mp, N, K, KS, KW, gelu_col_begin;
   unsigned int *status;
   unsigned long long limit_ns;
 };
@@ -59,9 +61,9 @@ __device__ __forceinline__ bool elect_one() {
 __host__ __device__ constexpr uint32_t idesc_mxf8(int m, int n) {
   return (1u << 23) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
-// ... with byte `id` of both scale words (B's id at bit 4, A's at bit 29).
-__device__ __forceinline__ uint32_t with_scale_byte(uint32_t idesc, uint32_t id) {
-  return idesc | (id << 4) | (id << 29);
+// ... with byte `a` of A's scale words (bit 29) and byte `b` of B's (bit 4).
+__device__ __forceinline__ uint32_t with_scale_bytes(uint32_t idesc, uint32_t a, uint32_t b) {
+  return idesc | (b << 4) | (a << 29);
 }
 
 __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -96,15 +98,15 @@ __device__ __forceinline__ float2 activate2(float2 y) {
 // [start[e], start[e + 1]) and token tiles [tiles[e], tiles[e + 1]).  Offsets
 // are taken as they come and clamped: into [0, M], and never below an earlier
 // one, so whatever they hold, the experts' rows are disjoint and inside Y.
-// Token tiles start at a multiple of 8 rows (where operand rows may start),
-// at or before the expert's first row.
+// Token tiles start at the expert's first row rounded down to a multiple of
+// `align` (8 where operand rows come from the quantized layout).
 struct ExpertTable {
   int start[FP8_MAX_EXPERTS + 1];
   int tiles[FP8_MAX_EXPERTS + 1];
 };
 
 // Fills the table; called by one full warp.
-__device__ __forceinline__ void fill_expert_table(const Params &p, int tile_rows, ExpertTable *t) {
+__device__ __forceinline__ void fill_expert_table(const Params &p, int tile_rows, int align, ExpertTable *t) {
   const int lane = threadIdx.x & 31;
   if (p.offsets == nullptr) {
     if (lane == 0) {
@@ -128,7 +130,7 @@ __device__ __forceinline__ void fill_expert_table(const Params &p, int tile_rows
     }
     int start = __shfl_up_sync(0xFFFFFFFFu, end, 1);
     if (lane == 0) start = first;
-    const int mine = e < p.experts && end > start ? (end - (start & ~7) + tile_rows - 1) / tile_rows : 0;
+    const int mine = e < p.experts && end > start ? (end - (start & -align) + tile_rows - 1) / tile_rows : 0;
     int sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -148,13 +150,16 @@ __device__ __forceinline__ void fill_expert_table(const Params &p, int tile_rows
   }
 }
 
-// A unit of work: the token tile [row0, row0 + tile_rows) of an expert against weight tile nt.  Rows below
-// `begin` or from `end` on belong to others.  An expert's units are consecutive, its token tiles fastest:
-// the units that share a weight tile run at the same time and read it from DRAM once.
+// A unit of work: the token tile [row0, row0 + tile_rows) of an expert against tile nt of the output columns.
+// Rows below `begin` or from `end` on belong to others.  An expert's units are consecutive, in panels of kPanel
+// column tiles, the panel's columns fastest: the units that run at the same time form a block of about as many
+// token tiles as column tiles, and read few distinct operand rows.
+constexpr int kPanel = 8;
 struct Item {
   int expert, nt, row0, begin, end;
 };
-__device__ __forceinline__ Item find_item(const Params &p, const ExpertTable *t, int tile_rows, int nt_count, int item) {
+__device__ __forceinline__ Item find_item(const Params &p, const ExpertTable *t, int tile_rows, int align,
+                                          int nt_count, int item) {
   int lo = 0, hi = p.experts;                         // the last expert whose first unit is <= item
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -162,13 +167,15 @@ __device__ __forceinline__ Item find_item(const Params &p, const ExpertTable *t,
     else hi = mid;
   }
   const int mts = t->tiles[lo + 1] - t->tiles[lo];
-  const int r = item - t->tiles[lo] * nt_count;
+  int r = item - t->tiles[lo] * nt_count;
+  const int panel = r / (kPanel * mts), width = min(kPanel, nt_count - panel * kPanel);
+  r -= panel * kPanel * mts;
   Item it;
   it.expert = lo;
-  it.nt = r / mts;
+  it.nt = panel * kPanel + r % width;
   it.begin = t->start[lo];
   it.end = t->start[lo + 1];
-  it.row0 = (it.begin & ~7) + (r % mts) * tile_rows;
+  it.row0 = (it.begin & -align) + (r / width) * tile_rows;
   return it;
 }
 

@@ -1,43 +1,19 @@
 // Block-scaled FP8 operands: the activation quantizer and the weight pack.
 //
-// Per row (an activation row, or an output column of the weight) and 128
-// elements along K:
-//   amax = largest finite |x|,  s = 2^e with the smallest e >= -127 such that
-//   amax <= 448 * 2^e,          code = e4m3(x / s), round to nearest even.
-// s is a power of two, so x / s is exact and the code carries the only
-// rounding (relative 2^-4 of a normal code); nothing saturates.  A power of
-// two instead of amax / 448 costs no precision (e4m3 codes keep their relative
-// step over 2^-6..448) and is what the tensor cores take as a block scale, so
-// the GEMM needs no rescaling pass.  Infinities and NaN become the NaN code: an
-// e4m3 has no infinity, and the row's products are NaN either way.
+// Both quantize blocks of 128 elements along K (fp8_quant.cuh): of an
+// activation row, and of an output column of the weight.
 #include <cuda_runtime.h>
 
 #include <string>
 
 #include "device_common.cuh"
 #include "fp8_layout.h"
+#include "fp8_quant.cuh"
 #include "svdq_internal.h"
 
 namespace svdq {
 namespace fp8 {
 namespace {
-
-// e4m3 codes of two values, the first in the low byte (RNE, satfinite; NaN gives the NaN code).
-__device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ float nan_if_infinite(float v) {
-  return fabsf(v) == __uint_as_float(0x7F800000u) ? __uint_as_float(0x7FC00000u) : v;
-}
-// |x| of both bf16 halves of a word as integers; non-finite halves become 0.
-__device__ __forceinline__ uint32_t finite_abs2(uint32_t w) {
-  uint32_t lo = w & 0x7FFFu, hi = (w >> 16) & 0x7FFFu;
-  lo = lo >= 0x7F80u ? 0u : lo;
-  hi = hi >= 0x7F80u ? 0u : hi;
-  return lo | (hi << 16);
-}
 
 // One warp per (row, scale word): 512 elements, 16 per lane, so 8 lanes hold a
 // block of 128.  Two 16-byte loads and one 16-byte store per lane.
@@ -60,40 +36,8 @@ __global__ void __launch_bounds__(QUANT_THREADS)
     v[0] = k0 < K ? __ldg(reinterpret_cast<const uint4 *>(src)) : make_uint4(0, 0, 0, 0);
     v[1] = k0 + 8 < K ? __ldg(reinterpret_cast<const uint4 *>(src + 8)) : make_uint4(0, 0, 0, 0);
     const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
-    uint32_t m2 = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m2 = __vmaxu2(m2, w[i] & 0x7FFF7FFFu);
-    uint32_t top = max(m2 & 0xFFFFu, m2 >> 16);
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    const bool odd = top >= 0x7F80u;          // a non-finite element in this block of 128
-    if (__any_sync(0xFFFFFFFFu, odd)) {       // rare: the maximum again, over the finite elements
-      uint32_t f2 = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f2 = __vmaxu2(f2, finite_abs2(w[i]));
-      uint32_t fin = max(f2 & 0xFFFFu, f2 >> 16);
-#pragma unroll
-      for (int o = 4; o > 0; o >>= 1) fin = max(fin, __shfl_xor_sync(0xFFFFFFFFu, fin, o));
-      top = fin;
-    }
-    const uint32_t byte = scale_byte(top << 16);
-    const float inv = inverse_scale(byte);
     uint32_t out[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float f[4];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        f[2 * j] = __uint_as_float(w[2 * i + j] << 16);
-        f[2 * j + 1] = __uint_as_float(w[2 * i + j] & 0xFFFF0000u);
-      }
-      if (odd) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) f[j] = nan_if_infinite(f[j]);
-      }
-      out[i] = cvt_e4m3x2(__fmul_rn(f[0], inv), __fmul_rn(f[1], inv)) |
-               (cvt_e4m3x2(__fmul_rn(f[2], inv), __fmul_rn(f[3], inv)) << 16);
-    }
+    const uint32_t byte = quantize16(w, out);
     const int ks = kw * 4 + (lane >> 3), chunk = lane & 7;
     if (ks < KS)
       *reinterpret_cast<uint4 *>(codes + (static_cast<size_t>(ks) * Mp + row) * kBlock + ((chunk ^ (row & 7)) << 4)) =
@@ -109,26 +53,28 @@ __global__ void __launch_bounds__(QUANT_THREADS)
 // per output column, which reads its 128 elements down K (a warp's reads of one
 // k are 64 contiguous bytes) and keeps them in registers between the maximum
 // and the codes.  Run once per layer.
-__global__ void __launch_bounds__(kTileN)
-    pack_weights_kernel(const uint16_t *W, int K, int N, size_t ldw, size_t stride_e, int KS, int KW, int NT,
-                        uint8_t *codes, uint8_t *scales) {
-  const int ks = blockIdx.x, nt = blockIdx.y, e = blockIdx.z;
-  const int r = threadIdx.x, n = nt * kTileN + r;
+constexpr int PACK_COLS = 128;
+
+__global__ void __launch_bounds__(PACK_COLS)
+    pack_weights_kernel(const uint16_t *W, int K, int N, size_t ldw, size_t stride_e, int KS, int KW, uint8_t *codes,
+                        uint8_t *scales) {
+  const int ks = blockIdx.x, e = blockIdx.z;
+  const int n = blockIdx.y * PACK_COLS + threadIdx.x;
+  if (n >= N) return;
   const uint16_t *src = W + static_cast<size_t>(e) * stride_e + n;
   uint32_t w[64];
   uint32_t m2 = 0;
 #pragma unroll
   for (int i = 0; i < 64; ++i) {
-    const int k = ks * kBlock + 2 * i;
-    const uint32_t lo = n < N && k < K ? __ldg(src + static_cast<size_t>(k) * ldw) : 0u;
-    const uint32_t hi = n < N && k + 1 < K ? __ldg(src + static_cast<size_t>(k + 1) * ldw) : 0u;
+    const int k = ks * kBlock + 2 * i;           // K % 8 == 0: both or neither
+    const uint32_t lo = k < K ? __ldg(src + static_cast<size_t>(k) * ldw) : 0u;
+    const uint32_t hi = k < K ? __ldg(src + static_cast<size_t>(k + 1) * ldw) : 0u;
     w[i] = lo | (hi << 16);
     m2 = __vmaxu2(m2, finite_abs2(w[i]));
   }
   const uint32_t byte = scale_byte(max(m2 & 0xFFFFu, m2 >> 16) << 16);
   const float inv = inverse_scale(byte);
-  const size_t tile = static_cast<size_t>(e) * NT + nt;
-  uint8_t *dst = codes + (tile * KS + ks) * kTileBytes + r * kBlock;
+  uint8_t *dst = codes + ((static_cast<size_t>(e) * KS + ks) * N + n) * kBlock;
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
     uint32_t out[4];
@@ -141,30 +87,18 @@ __global__ void __launch_bounds__(kTileN)
                            __fmul_rn(nan_if_infinite(__uint_as_float(b & 0xFFFF0000u)), inv))
                 << 16);
     }
-    *reinterpret_cast<uint4 *>(dst + ((c ^ (r & 7)) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
+    *reinterpret_cast<uint4 *>(dst + ((c ^ (n & 7)) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
   }
-  uint8_t *atom = scales + (tile * KW + ks / 4) * kScaleAtom + (r & 31) * 16 + (r >> 5) * 4;
-  atom[ks & 3] = static_cast<uint8_t>(byte);
-  if (ks == KS - 1)                            // the blocks past K of the last word
-    for (int j = (ks & 3) + 1; j < 4; ++j) atom[j] = 127;
-}
-
-int check_rows(const char *fn, const void *X, int M, int K, int ldx, const void *workspace) {
-  const std::string name(fn);
-  if (!X || !workspace) return fail(SVDQ_ERR_INVALID_ARG, name + ": null pointer");
-  if (M < 1 || K < 8 || K % 8 || ldx < K || ldx % 8)
-    return fail(SVDQ_ERR_SHAPE, name + ": need M >= 1, K % 8 == 0, ldx >= K, ldx % 8 == 0");
-  if (!aligned16(X) || !aligned16(workspace))
-    return fail(SVDQ_ERR_ALIGNMENT, name + ": pointers must be 16-byte aligned");
-  return SVDQ_OK;
+  uint8_t *word = scales + ((static_cast<size_t>(e) * KW + ks / 4) * N + n) * 4;
+  word[ks & 3] = static_cast<uint8_t>(byte);
+  if (ks == KS - 1)                              // the blocks past K of the last word
+    for (int j = (ks & 3) + 1; j < 4; ++j) word[j] = 127;
 }
 
 }  // namespace
 
 int launch_quantize_act(const char *fn, const void *X, int M, int K, int ldx, void *workspace, int sm_count,
                         cudaStream_t stream) {
-  int rc = check_rows(fn, X, M, K, ldx, workspace);
-  if (rc != SVDQ_OK) return rc;
   const int KS = k_stages(K), KW = k_words(K), Mp = padded_rows(M);
   const long long total = static_cast<long long>(M) * KW;
   const long long blocks = (total + QUANT_THREADS / 32 - 1) / (QUANT_THREADS / 32);
@@ -192,10 +126,11 @@ extern "C" int fp8_weight_size(int K, int N, int experts, size_t *bytes) {
   return ok();
 }
 
-extern "C" int fp8_workspace_size(int M, int K, size_t *bytes) {
+extern "C" int fp8_workspace_size(int M, int K, int experts, size_t *bytes) {
   if (!bytes) return fail(SVDQ_ERR_INVALID_ARG, "fp8_workspace_size: null pointer");
-  if (M < 1 || K < 8 || K % 8) return fail(SVDQ_ERR_SHAPE, "fp8_workspace_size: need M >= 1, K % 8 == 0");
-  *bytes = fp8::act_bytes(M, K);
+  if (M < 1 || K < 8 || K % 8 || experts < 1 || experts > FP8_MAX_EXPERTS)
+    return fail(SVDQ_ERR_SHAPE, "fp8_workspace_size: need M >= 1, K % 8 == 0, 1 <= experts <= 512");
+  *bytes = fp8::needs_workspace(M, experts) ? fp8::act_bytes(M, K) : 0;
   return ok();
 }
 
@@ -203,27 +138,18 @@ extern "C" int fp8_pack_weights(const void *W, int K, int N, int ldw, int64_t ex
                                 svdq_stream_t stream) {
   if (!W || !packed) return fail(SVDQ_ERR_INVALID_ARG, "fp8_pack_weights: null pointer");
   if (K < 8 || K % 8 || N < 8 || N % 8 || experts < 1 || experts > FP8_MAX_EXPERTS || ldw < N ||
-      (experts > 1 && expert_stride < 0) || fp8::n_tiles(N) > 65535)
+      (experts > 1 && expert_stride < 0) || N > 8388480)
     return fail(SVDQ_ERR_SHAPE,
                 "fp8_pack_weights: need K % 8 == 0, N % 8 == 0, N <= 8388480, ldw >= N, 1 <= experts <= 512");
   if (!aligned16(packed)) return fail(SVDQ_ERR_ALIGNMENT, "fp8_pack_weights: packed must be 16-byte aligned");
   if (!current_device_state()) return SVDQ_ERR_NOT_INITIALIZED;
-  const int KS = fp8::k_stages(K), KW = fp8::k_words(K), NT = fp8::n_tiles(N);
+  const int KS = fp8::k_stages(K), KW = fp8::k_words(K);
+  const int blocks_n = (N + fp8::PACK_COLS - 1) / fp8::PACK_COLS;
   uint8_t *codes = static_cast<uint8_t *>(packed);
-  fp8::pack_weights_kernel<<<dim3(KS, NT, experts), fp8::kTileN, 0, stream>>>(
-      static_cast<const uint16_t *>(W), K, N, static_cast<size_t>(ldw), static_cast<size_t>(expert_stride), KS, KW, NT,
+  fp8::pack_weights_kernel<<<dim3(KS, blocks_n, experts), fp8::PACK_COLS, 0, stream>>>(
+      static_cast<const uint16_t *>(W), K, N, static_cast<size_t>(ldw), static_cast<size_t>(expert_stride), KS, KW,
       codes, codes + fp8::weight_code_bytes(K, N, experts));
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(SVDQ_ERR_CUDA, std::string("fp8_pack_weights launch: ") + cudaGetErrorString(e));
   return ok();
-}
-
-extern "C" int fp8_quantize_act(const void *X, int M, int K, int ldx, void *workspace, svdq_stream_t stream) {
-  // arguments are judged before the device, like every other device call
-  int rc = fp8::check_rows("fp8_quantize_act", X, M, K, ldx, workspace);
-  if (rc != SVDQ_OK) return rc;
-  DeviceState *st = current_device_state();
-  if (!st) return SVDQ_ERR_NOT_INITIALIZED;
-  rc = fp8::launch_quantize_act("fp8_quantize_act", X, M, K, ldx, workspace, st->sm_count, stream);
-  return rc == SVDQ_OK ? ok() : rc;
 }

@@ -11,8 +11,6 @@ their workspaces and outputs come from torch's allocator, on the stream the
 call runs on, so an instance may be used from several streams and captured
 into several graphs.
 """
-import ctypes
-
 import numpy as np
 import torch
 
@@ -332,18 +330,18 @@ class AWQLinear:
         return Y
 
 
-def _on(device, stream, call):
-    """call(raw stream) with `device` current and torch allocating on the stream the work runs on: `stream`, else
-    the caller's current stream of that device."""
+def _on(device, stream, call, *args):
+    """call(*args, raw stream) with `device` current and torch allocating on the stream the work runs on: `stream`,
+    else the caller's current stream of that device."""
     if stream is not None:
         if stream.device != device:
             raise ValueError(f"the stream is on {stream.device}, the layer on {device}")
         with torch.cuda.stream(stream):       # makes the stream's device current as well
-            return call(stream.cuda_stream)
+            return call(*args, stream.cuda_stream)
     if torch.cuda.current_device() == device.index:
-        return call(_raw_stream(None, device))
+        return call(*args, _raw_stream(None, device))
     with torch.cuda.device(device):
-        return call(_raw_stream(None, device))
+        return call(*args, _raw_stream(None, device))
 
 
 class FP8Linear:
@@ -385,38 +383,45 @@ class FP8Linear:
         bias = None if bias_bits is None else _dev(bias_bits, device, torch.bfloat16)
         return cls(_dev(W_bits, device, torch.bfloat16), bias, epilogue, gelu_col_begin)
 
-    def _run(self, X, offsets, Y, stream):
+    def _call(self, X, offsets, Y, s):
+        """The checked call on raw stream `s`, which torch allocates on."""
         name = type(self).__name__
-        _check_input(X, self.K, self.device, name)
-        M = X.shape[0]
-        if X.stride(1) != 1:
+        shape, K, N = X.shape, self.K, self.N
+        if len(shape) != 2 or shape[1] != K:
+            raise ValueError(f"{name}: X must be [M, {K}], got {tuple(shape)}")
+        if X.dtype is not torch.bfloat16 or X.device != self.device:
+            raise ValueError(f"{name}: X must be bf16 on {self.device}, got {X.dtype} on {X.device}")
+        ldx, step = X.stride()
+        if step != 1:
             raise ValueError(f"{name}: X must have unit stride in its last dimension")
-        if Y is not None:
-            _check_output(Y, M, self.N, self.device, name)
-            if Y.stride(1) != 1:
+        M, ldy = shape[0], N
+        if Y is None:
+            Y = X.new_empty((M, N)) if offsets is None else X.new_zeros((M, N))
+        else:
+            _check_output(Y, M, N, self.device, name)
+            ldy, step = Y.stride()
+            if step != 1:
                 raise ValueError(f"{name}: Y must have unit stride in its last dimension")
-
-        def call(s):
-            out = Y if Y is not None else torch.empty((M, self.N), dtype=torch.bfloat16, device=self.device)
-            ws = torch.empty(lib.fp8_workspace_size(M, self.K), dtype=torch.uint8, device=self.device)
-            ldx, ldy = (X.stride(0), out.stride(0)) if M > 1 else (self.K, self.N)
-            bias = None if self.bias is None else self.bias.data_ptr()
-            L = lib.load()
-            if offsets is None:
-                lib._check("fp8_linear", L.fp8_linear(
-                    X.data_ptr(), M, self.K, ldx, self.packed.data_ptr(), bias, self.N, self.epilogue,
-                    self.gelu_col_begin, out.data_ptr(), ldy, ws.data_ptr(), s))
-            else:
-                lib._check("fp8_linear_grouped", L.fp8_linear_grouped(
-                    X.data_ptr(), M, self.K, ldx, offsets.data_ptr(), self.experts, self.packed.data_ptr(), bias,
-                    self.N, self.epilogue, self.gelu_col_begin, out.data_ptr(), ldy, ws.data_ptr(), s))
-            return out
-
-        return _on(self.device, stream, call)
+        if M == 1:                                # a single row's stride is its width, whatever torch recorded
+            ldx, ldy = K, N
+        experts = self.experts or 1
+        need = lib.fp8_workspace_size(M, K, experts)
+        ws = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
+        bias = self.bias
+        args = (self.packed.data_ptr(), None if bias is None else bias.data_ptr(), N, self.epilogue,
+                self.gelu_col_begin, Y.data_ptr(), ldy, None if ws is None else ws.data_ptr(), s)
+        L = lib.load()
+        if offsets is None:
+            rc = L.fp8_linear(X.data_ptr(), M, K, ldx, *args)
+        else:
+            rc = L.fp8_linear_grouped(X.data_ptr(), M, K, ldx, offsets.data_ptr(), experts, *args)
+        if rc:
+            lib._check("fp8_linear" if offsets is None else "fp8_linear_grouped", rc)
+        return Y
 
     def __call__(self, X, Y=None, stream=None):
         """X: bf16 CUDA [M, K] -> bf16 [M, N] (into Y if given)."""
-        return self._run(X, None, Y, stream)
+        return _on(self.device, stream, self._call, X, None, Y)
 
 
 class FP8Experts(FP8Linear):
@@ -436,10 +441,7 @@ class FP8Experts(FP8Linear):
                 or offsets.device != self.device or not offsets.is_contiguous()):
             raise ValueError(f"FP8Experts: offsets must be contiguous int32 [{self.experts + 1}] on {self.device}, got "
                              f"{offsets.dtype} {tuple(offsets.shape)} on {offsets.device}")
-        if Y is None:
-            Y = _on(self.device, stream, lambda s: torch.zeros((X.shape[0], self.N), dtype=torch.bfloat16,
-                                                               device=self.device))
-        return self._run(X, offsets, Y, stream)
+        return _on(self.device, stream, self._call, X, offsets, Y)
 
 
 class RotaryND:
@@ -473,21 +475,22 @@ class RotaryND:
     def __call__(self, q, k, pos, q_out=None, k_out=None, inverse=False, stream=None):
         """q: bf16 CUDA [M, heads, D] (any row and head strides), k likewise or None; pos: int32 or float32
         [M, axes].  Returns (q_out, k_out); q_out may be q, k_out may be k.  inverse: turns back."""
+        return _on(self.device, stream, self._call, q, k, pos, q_out, k_out, inverse)
+
+    def _call(self, q, k, pos, q_out, k_out, inverse, s):
+        device = self.device
         if q.dim() != 3 or pos.dim() != 2 or pos.shape[0] != q.shape[0]:
             raise ValueError(f"RotaryND: q must be [M, heads, {self.D}] and pos [M, {self.axes}], got "
                              f"{tuple(q.shape)} and {tuple(pos.shape)}")
         if k is None and k_out is not None:
             raise ValueError("RotaryND: k_out without k")
         for t in (q, k, pos, q_out, k_out):
-            if t is not None and t.device != self.device:
-                raise ValueError(f"RotaryND: every tensor must be on {self.device}, got {t.device}")
-
-        def call(s):
-            qo = q_out if q_out is not None else torch.empty(q.shape, dtype=torch.bfloat16, device=self.device)
-            ko = k_out if k_out is not None or k is None else torch.empty(k.shape, dtype=torch.bfloat16,
-                                                                          device=self.device)
-            lib.rope_nd(q, k, self.plan, pos, qo, ko, self.q_norm, self.k_norm if k is not None else None, inverse,
-                        self.eps, ctypes.c_void_p(s))
-            return qo, ko
-
-        return _on(self.device, stream, call)
+            if t is not None and t.device != device:
+                raise ValueError(f"RotaryND: every tensor must be on {device}, got {t.device}")
+        if q_out is None:
+            q_out = q.new_empty(q.shape)
+        if k_out is None and k is not None:
+            k_out = k.new_empty(k.shape)
+        lib.rope_nd(q, k, self.plan, pos, q_out, k_out, self.q_norm, None if k is None else self.k_norm, inverse,
+                    self.eps, s)
+        return q_out, k_out

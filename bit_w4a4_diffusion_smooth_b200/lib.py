@@ -8,6 +8,7 @@ arrays.  A missing library raises immediately: there is no fallback path.
 import ctypes
 import functools
 import os
+import struct
 
 import numpy as np
 
@@ -70,11 +71,9 @@ class RopePlan(ctypes.Structure):
                 ("axis", ctypes.c_ubyte * 128), ("freq", ctypes.c_double * 128)]
 
 
-class RopeTensor(ctypes.Structure):
-    """rope_nd_tensor of include/svdq.h."""
-    _fields_ = [("X", ctypes.c_void_p), ("x_row", ctypes.c_int64), ("x_head", ctypes.c_int64), ("Y", ctypes.c_void_p),
-                ("y_row", ctypes.c_int64), ("y_head", ctypes.c_int64), ("norm", ctypes.c_void_p),
-                ("heads", ctypes.c_int)]
+# rope_nd_tensor of include/svdq.h: X, x_row, x_head, Y, y_row, y_head, norm, heads (packed bytes marshal
+# faster than a ctypes structure, and the call takes them by address all the same).
+ROPE_TENSOR = struct.Struct("@PqqPqqPi4x")
 
 
 _SIGNATURES = {
@@ -113,13 +112,12 @@ _SIGNATURES = {
     "awq_expand_weights": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _P]),
     "awq_linear_w4a16_expanded": (_I, [_P, _I, _I, _I, _P, _I, _P, _I, _P, _P]),
     "fp8_weight_size": (_I, [_I, _I, _I, _SZ]),
-    "fp8_workspace_size": (_I, [_I, _I, _SZ]),
+    "fp8_workspace_size": (_I, [_I, _I, _I, _SZ]),
     "fp8_pack_weights": (_I, [_P, _I, _I, _I, ctypes.c_int64, _I, _P, _P]),
-    "fp8_quantize_act": (_I, [_P, _I, _I, _I, _P, _P]),
     "fp8_linear": (_I, [_P, _I, _I, _I, _P, _P, _I, _I, _I, _P, _I, _P, _P]),
     "fp8_linear_grouped": (_I, [_P, _I, _I, _I, _P, _I, _P, _P, _I, _I, _I, _P, _I, _P, _P]),
-    "rope_nd": (_I, [ctypes.POINTER(RopeTensor), ctypes.POINTER(RopeTensor), _I, ctypes.POINTER(RopePlan), _P,
-                     ctypes.c_int64, _I, _I, ctypes.c_float, _P]),
+    "rope_nd": (_I, [ctypes.c_char_p, ctypes.c_char_p, _I, ctypes.POINTER(RopePlan), _P, ctypes.c_int64, _I, _I,
+                     ctypes.c_float, _P]),
     "svdq_check_status": (_I, [_P]),
     "svdq_debug_wait_timeout": (_I, [ctypes.c_uint64, _P]),
     "svdq_debug_convert": (_I, [_P, _I, _P, _P, _P]),
@@ -176,13 +174,6 @@ def _dptr(t, name, dtype=None, allow_none=False):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _dptr_any(t, name):
-    """Device pointer of a CUDA tensor of any type and strides."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return ctypes.c_void_p(t.data_ptr())
-
-
 def _nbytes(t):
     return t.numel() * t.element_size()
 
@@ -201,7 +192,7 @@ def _need_2d(t, rows, cols, name):
 
 def _stream(stream):
     import torch
-    if isinstance(stream, ctypes.c_void_p):     # a raw handle
+    if isinstance(stream, int):     # a raw handle
         return stream
     s = stream if stream is not None else torch.cuda.current_stream()
     return ctypes.c_void_p(s.cuda_stream)
@@ -711,10 +702,10 @@ def fp8_weight_size(K, N, experts=1):
 
 
 @functools.lru_cache(maxsize=1024)
-def fp8_workspace_size(M, K):
-    """Bytes of the workspace of an FP8 call with M rows (cached per shape)."""
+def fp8_workspace_size(M, K, experts=1):
+    """Bytes of the workspace of an FP8 call with M rows, 0 where it needs none (cached per shape)."""
     n = ctypes.c_size_t()
-    _check("fp8_workspace_size", load().fp8_workspace_size(M, K, ctypes.byref(n)))
+    _check("fp8_workspace_size", load().fp8_workspace_size(M, K, experts, ctypes.byref(n)))
     return n.value
 
 
@@ -740,39 +731,38 @@ def fp8_pack_weights(W, packed=None, stream=None):
     return packed
 
 
-def fp8_quantize_act(X, workspace, stream=None):
-    """Enqueues the FP8 activation quantizer.  X: bf16 CUDA [M, K] (row stride ldx)."""
+def _fp8_workspace(workspace, M, K, experts):
+    """Device pointer of an FP8 call's workspace (None where the call needs none)."""
     import torch
-    M, K = X.shape
-    _need_bytes(workspace, fp8_workspace_size(M, K), "workspace")
-    _check("fp8_quantize_act", load().fp8_quantize_act(
-        _dptr(X, "X", torch.bfloat16), M, K, _row_stride(X, K), _dptr(workspace, "workspace", torch.uint8),
-        _stream(stream)))
+    need = fp8_workspace_size(M, K, experts)
+    if need == 0:
+        return None
+    if workspace is None:
+        raise ValueError("workspace is required")
+    _need_bytes(workspace, need, "workspace")
+    return _dptr(workspace, "workspace", torch.uint8)
 
 
-def fp8_linear(X, packed, bias, N, epilogue, gelu_col_begin, Y, workspace, stream=None):
+def fp8_linear(X, packed, bias, N, epilogue, gelu_col_begin, Y, workspace=None, stream=None):
     """Enqueues the FP8 linear layer.  X: bf16 CUDA [M, K]; Y: bf16 CUDA [M, N] (row strides ldx, ldy)."""
     import torch
     M, K = X.shape
     _need_bytes(packed, fp8_weight_size(K, N), "packed")
-    _need_bytes(workspace, fp8_workspace_size(M, K), "workspace")
     _need_bytes(bias, 2 * N, "bias")
     _need_2d(Y, M, N, "Y")
     _check("fp8_linear", load().fp8_linear(
         _dptr(X, "X", torch.bfloat16), M, K, _row_stride(X, K), _dptr(packed, "packed", torch.uint8),
         _dptr(bias, "bias", torch.bfloat16, allow_none=True), N, epilogue, gelu_col_begin,
-        _dptr(Y, "Y", torch.bfloat16), _row_stride(Y, N), _dptr(workspace, "workspace", torch.uint8),
-        _stream(stream)))
+        _dptr(Y, "Y", torch.bfloat16), _row_stride(Y, N), _fp8_workspace(workspace, M, K, 1), _stream(stream)))
 
 
-def fp8_linear_grouped(X, offsets, packed, bias, N, epilogue, gelu_col_begin, Y, workspace, stream=None):
+def fp8_linear_grouped(X, offsets, packed, bias, N, epilogue, gelu_col_begin, Y, workspace=None, stream=None):
     """Enqueues the FP8 product by expert.  X: bf16 CUDA [M, K]; offsets: int32 CUDA [experts + 1]; bias: bf16
     CUDA [experts, N] or None; Y: bf16 CUDA [M, N]."""
     import torch
     M, K = X.shape
     E = offsets.numel() - 1
     _need_bytes(packed, fp8_weight_size(K, N, E), "packed")
-    _need_bytes(workspace, fp8_workspace_size(M, K), "workspace")
     _need_bytes(bias, 2 * N * E, "bias")
     _need_2d(Y, M, N, "Y")
     if offsets.dim() != 1 or not offsets.is_contiguous() or (bias is not None and not bias.is_contiguous()):
@@ -781,45 +771,53 @@ def fp8_linear_grouped(X, offsets, packed, bias, N, epilogue, gelu_col_begin, Y,
         _dptr(X, "X", torch.bfloat16), M, K, _row_stride(X, K), _dptr(offsets, "offsets", torch.int32), E,
         _dptr(packed, "packed", torch.uint8), _dptr(bias, "bias", torch.bfloat16, allow_none=True), N, epilogue,
         gelu_col_begin, _dptr(Y, "Y", torch.bfloat16), _row_stride(Y, N),
-        _dptr(workspace, "workspace", torch.uint8), _stream(stream)))
+        _fp8_workspace(workspace, M, K, E), _stream(stream)))
 
 
 def _rope_tensor(x, y, norm, M, D, name):
-    """Checks one tensor's heads [M, heads, D] and returns its RopeTensor."""
+    """Checks one tensor's heads [M, heads, D] and returns its packed rope_nd_tensor."""
     import torch
-    if x.dim() != 3 or x.shape[0] != M or x.shape[2] != D or tuple(y.shape) != tuple(x.shape):
+    shape = x.shape
+    if len(shape) != 3 or shape[0] != M or shape[2] != D or y.shape != shape:
         raise ValueError(f"{name} must be [{M}, heads, {D}] and its output alike, got {tuple(x.shape)} and "
                          f"{tuple(y.shape)}")
     if x.dtype is not torch.bfloat16 or y.dtype is not torch.bfloat16:
         raise ValueError(f"{name} must have dtype {torch.bfloat16}, got {x.dtype} and {y.dtype}")
     if not (x.is_cuda and y.is_cuda):
         raise ValueError(f"{name} must be a CUDA tensor")
-    H = x.shape[1]
-    xs, ys = x.stride(), y.stride()
-    if xs[2] != 1 or ys[2] != 1:
+    H = shape[1]
+    (xr, xh, xd), (yr, yh, yd) = x.stride(), y.stride()
+    if xd != 1 or yd != 1:
         raise ValueError(f"{name} must have unit stride in its last dimension")
-    return RopeTensor(x.data_ptr(), xs[0] if M > 1 else 0, xs[1] if H > 1 else 0, y.data_ptr(), ys[0] if M > 1 else 0,
-                      ys[1] if H > 1 else 0, None if norm is None else norm.data_ptr(), H)
+    if M <= 1:
+        xr = yr = 0
+    if H <= 1:
+        xh = yh = 0
+    return ROPE_TENSOR.pack(x.data_ptr(), xr, xh, y.data_ptr(), yr, yh, 0 if norm is None else norm.data_ptr(), H)
 
 
 def rope_nd(q, k, plan, pos, q_out, k_out, q_norm=None, k_norm=None, inverse=False, eps=1e-6, stream=None):
     """Enqueues the rotary positions of q [M, heads, D] and k (likewise, or None), bf16 CUDA, into q_out and
     k_out (which may be q and k).  pos: int32 or float32 CUDA [M, axes]; norms: bf16 CUDA [D] or None."""
     import torch
-    M, D = pos.shape[0], plan.D
-    if pos.dim() != 2 or pos.shape[1] != plan.axes or (plan.axes > 1 and pos.stride(1) != 1):
-        raise ValueError(f"pos must be [M, {plan.axes}] with unit stride in its last dimension, got {tuple(pos.shape)}")
-    if pos.dtype not in (torch.int32, torch.float32):
+    D, axes = plan.D, plan.axes
+    if pos.dim() != 2 or pos.shape[1] != axes or (axes > 1 and pos.stride(1) != 1):
+        raise ValueError(f"pos must be [M, {axes}] with unit stride in its last dimension, got {tuple(pos.shape)}")
+    if pos.dtype is not torch.int32 and pos.dtype is not torch.float32:
         raise ValueError(f"pos must be int32 or float32, got {pos.dtype}")
+    if not pos.is_cuda:
+        raise ValueError("pos must be a CUDA tensor")
     for norm in (q_norm, k_norm):
         if norm is not None and (norm.dtype is not torch.bfloat16 or norm.numel() != D or not norm.is_contiguous()
                                  or not norm.is_cuda):
             raise ValueError(f"a norm weight must be bf16 CUDA [{D}]")
+    M = pos.shape[0]
     tq = _rope_tensor(q, q_out, q_norm, M, D, "q")
-    tk = None if k is None else ctypes.byref(_rope_tensor(k, k_out, k_norm, M, D, "k"))
-    _check("rope_nd", load().rope_nd(
-        ctypes.byref(tq), tk, M, ctypes.byref(plan), _dptr_any(pos, "pos"), pos.stride(0) if M > 1 else 0,
-        pos.dtype is torch.float32, bool(inverse), eps, _stream(stream)))
+    tk = None if k is None else _rope_tensor(k, k_out, k_norm, M, D, "k")
+    rc = load().rope_nd(tq, tk, M, plan, pos.data_ptr(), pos.stride(0) if M > 1 else 0, pos.dtype is torch.float32,
+                        inverse, eps, _stream(stream))
+    if rc != OK:
+        _check("rope_nd", rc)
 
 
 def svdq_check_status(stream=None):

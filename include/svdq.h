@@ -555,13 +555,14 @@ int svdq_linear_int4(const uint8_t *a_codes, const void *a_scales, const void *U
  * Rules: K >= 8, K % 8 == 0, N >= 8, N % 8 == 0, 1 <= experts <= FP8_MAX_EXPERTS. */
 int fp8_weight_size(int K, int N, int experts, size_t *bytes);
 
-/* Bytes of the workspace of a call with M rows: the quantized activations.
- * Rules: M >= 1, K >= 8, K % 8 == 0. */
-int fp8_workspace_size(int M, int K, size_t *bytes);
+/* Bytes of the workspace of a call: the quantized activations, or 0 where the
+ * call quantizes them on the way in (an average share of at most 16 rows an
+ * expert).  Rules: M >= 1, K >= 8, K % 8 == 0, 1 <= experts <= FP8_MAX_EXPERTS. */
+int fp8_workspace_size(int M, int K, int experts, size_t *bytes);
 
 /*
  * Quantizes bf16 weights on the GPU into `packed` (fp8_weight_size bytes, an
- * opaque layout: swizzled tiles of 128 output columns x 128 k, then the scale
+ * opaque layout: codes stage by stage of 128 k, swizzled rows, then the scale
  * words).  W: `experts` matrices [K][ldw] bf16, expert_stride elements apart
  * (any alignment of a bf16 is enough here).
  * Rules: those of fp8_weight_size, ldw >= N, expert_stride >= 0.
@@ -570,24 +571,14 @@ int fp8_pack_weights(const void *W, int K, int N, int ldw, int64_t expert_stride
                      svdq_stream_t stream);
 
 /*
- * The activation quantizer of the two calls below, by itself.  workspace
- * (fp8_workspace_size(M, K) bytes) receives, with KS = ceil(K/128),
- * KW = ceil(KS/4) and Mp = M rounded up to 8: codes [KS][Mp][128] (16-byte
- * chunk c of row m at chunk c ^ (m % 8); 0 past K), then the scale words
- * [KW][Mp]: byte j of word (w, m) is e + 127 of block 4w + j.  Rows M..Mp-1 are
- * not written.
- * Rules: M >= 1, K >= 8, K % 8 == 0, ldx >= K, ldx % 8 == 0.
- */
-int fp8_quantize_act(const void *X, int M, int K, int ldx, void *workspace, svdq_stream_t stream);
-
-/*
- * The linear layer: quantizes X [M][ldx] bf16 into workspace and multiplies.
+ * The linear layer: quantizes X [M][ldx] bf16 and multiplies.
  * packed from fp8_pack_weights (experts = 1); bias [N] bf16 or NULL; the
  * epilogue's GELU applies from column gelu_col_begin on; Y [M][ldy] bf16.
- * workspace: fp8_workspace_size(M, K) bytes, in use until the call has run on
- * the stream (calls that may overlap take workspaces of their own).
- * Rules: those of fp8_quantize_act, N >= 8, N % 8 == 0, ldy >= N, ldy % 8 == 0,
- * 0 <= gelu_col_begin <= N.
+ * workspace: fp8_workspace_size(M, K, experts) bytes (NULL where that is 0), in
+ * use until the call has run on the stream (calls that may overlap take
+ * workspaces of their own).
+ * Rules: M >= 1, K >= 8, K % 8 == 0, ldx >= K, ldx % 8 == 0, N >= 8, N % 8 == 0,
+ * ldy >= N, ldy % 8 == 0, 0 <= gelu_col_begin <= N.
  */
 int fp8_linear(const void *X, int M, int K, int ldx, const void *packed, const void *bias, int N, int epilogue,
                int gelu_col_begin, void *Y, int ldy, void *workspace, svdq_stream_t stream);

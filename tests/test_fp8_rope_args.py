@@ -12,15 +12,17 @@ ODD = ctypes.c_void_p(24)
 
 
 def test_sizes():
-    # K = 136: two stages, one scale word; N = 136: two weight tiles; 9 rows take 16
-    assert lib.fp8_weight_size(136, 136, 3) == 3 * 2 * (2 * 16384 + 512)
-    assert lib.fp8_workspace_size(9, 136) == 2 * 16 * 128 + 16 * 4
-    assert lib.fp8_workspace_size(1, 8) == 8 * 128 + 8 * 4
+    # K = 136: two stages, one scale word; 1001 rows take 1008; few rows an expert need no workspace
+    assert lib.fp8_weight_size(136, 136, 3) == 3 * 136 * (2 * 128 + 4)
+    assert lib.fp8_workspace_size(1001, 136) == 2 * 1008 * 128 + 1008 * 4
+    assert lib.fp8_workspace_size(129, 8) == 136 * 128 + 136 * 4
+    assert lib.fp8_workspace_size(16, 136) == lib.fp8_workspace_size(128, 136, 8) == 0
+    assert lib.fp8_workspace_size(17, 136) > 0 and lib.fp8_workspace_size(129, 136, 8) > 0
     for bad in ((0, 8), (12, 8), (8, 0), (8, 12), (8, 8, 0), (8, 8, 513)):
         with pytest.raises(lib.SvdqError) as e:
             lib.fp8_weight_size(*bad)
         assert e.value.status == lib.ERR_SHAPE
-    for bad in ((0, 8), (1, 4), (1, 0), (-1, 8)):
+    for bad in ((0, 8), (1, 4), (1, 0), (-1, 8), (4, 8, 0), (4, 8, 513)):
         with pytest.raises(lib.SvdqError) as e:
             lib.fp8_workspace_size(*bad)
         assert e.value.status == lib.ERR_SHAPE
@@ -32,30 +34,26 @@ def _linear(x=P, M=4, K=64, ldx=64, w=P, bias=None, N=64, epi=0, begin=0, y=P, l
 
 @pytest.mark.parametrize("kw,want", [
     (dict(x=None), lib.ERR_INVALID_ARG), (dict(w=None), lib.ERR_INVALID_ARG), (dict(y=None), lib.ERR_INVALID_ARG),
-    (dict(ws=None), lib.ERR_INVALID_ARG), (dict(epi=3), lib.ERR_INVALID_ARG), (dict(epi=-1), lib.ERR_INVALID_ARG),
+    (dict(M=129, ws=None), lib.ERR_INVALID_ARG), (dict(epi=3), lib.ERR_INVALID_ARG), (dict(epi=-1), lib.ERR_INVALID_ARG),
     (dict(M=0), lib.ERR_SHAPE), (dict(M=-5), lib.ERR_SHAPE), (dict(K=60), lib.ERR_SHAPE), (dict(K=0), lib.ERR_SHAPE),
     (dict(N=60), lib.ERR_SHAPE), (dict(N=0), lib.ERR_SHAPE), (dict(ldx=56), lib.ERR_SHAPE), (dict(ldx=68), lib.ERR_SHAPE),
     (dict(ldy=56), lib.ERR_SHAPE), (dict(ldy=68), lib.ERR_SHAPE), (dict(begin=-1), lib.ERR_SHAPE),
     (dict(begin=65), lib.ERR_SHAPE), (dict(M=2 ** 31 - 1, N=2 ** 20, ldy=2 ** 20), lib.ERR_SHAPE),
     (dict(x=ODD), lib.ERR_ALIGNMENT), (dict(w=ODD), lib.ERR_ALIGNMENT), (dict(y=ODD), lib.ERR_ALIGNMENT),
-    (dict(ws=ODD), lib.ERR_ALIGNMENT)])
+    (dict(M=129, ws=ODD), lib.ERR_ALIGNMENT), (dict(bias=ODD), lib.ERR_ALIGNMENT)])
 def test_fp8_linear_refuses(kw, want):
     assert _linear(**kw) == want
 
 
-def test_fp8_grouped_pack_and_quantize_refuse():
+def test_fp8_grouped_and_pack_refuse():
     so = lib.load()
     g = lambda off=P, E=2, M=4: so.fp8_linear_grouped(P, M, 64, 64, off, E, P, None, 64, 0, 0, P, 64, P, None)
-    assert g(off=None) == lib.ERR_INVALID_ARG
+    assert g(off=None) == lib.ERR_INVALID_ARG and g(off=ctypes.c_void_p(18)) == lib.ERR_ALIGNMENT
     assert g(E=0) == lib.ERR_SHAPE and g(E=513) == lib.ERR_SHAPE and g(M=0) == lib.ERR_SHAPE
     k = lambda W=P, K=64, N=64, ldw=64, st=0, E=1, out=P: so.fp8_pack_weights(W, K, N, ldw, st, E, out, None)
     assert k(W=None) == lib.ERR_INVALID_ARG and k(out=None) == lib.ERR_INVALID_ARG and k(out=ODD) == lib.ERR_ALIGNMENT
     assert k(K=4) == lib.ERR_SHAPE and k(N=4) == lib.ERR_SHAPE and k(ldw=63) == lib.ERR_SHAPE
     assert k(E=0) == lib.ERR_SHAPE and k(E=2, st=-1) == lib.ERR_SHAPE
-    q = lambda X=P, M=4, K=64, ldx=64, ws=P: so.fp8_quantize_act(X, M, K, ldx, ws, None)
-    assert q(X=None) == lib.ERR_INVALID_ARG and q(ws=None) == lib.ERR_INVALID_ARG
-    assert q(M=0) == lib.ERR_SHAPE and q(K=4) == lib.ERR_SHAPE and q(ldx=60) == lib.ERR_SHAPE
-    assert q(X=ODD) == lib.ERR_ALIGNMENT and q(ws=ODD) == lib.ERR_ALIGNMENT
 
 
 def _plan(D=16, axes=2, pairing=0):
@@ -66,7 +64,7 @@ def _plan(D=16, axes=2, pairing=0):
 
 
 def _rope(q=None, k=None, M=4, plan=None, pos=P, row=2, inverse=0):
-    mk = lambda t: None if t is None else ctypes.byref(lib.RopeTensor(*t))
+    mk = lambda t: None if t is None else lib.ROPE_TENSOR.pack(*[0 if v is None else v for v in t])
     q = (16, 32, 16, 32, 32, 16, None, 2) if q is None else q
     plan = _plan() if plan is None else plan
     return lib.load().rope_nd(mk(q), mk(k), M, ctypes.byref(plan), pos, row, 0, inverse, 1e-6, None)

@@ -45,41 +45,34 @@ def close(got, want, mag, K, epilogue):
     assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4].tolist(), got[bad][:4], want[bad][:4])
 
 
-def unpack(ws, M, K):
-    """Workspace bytes -> (codes [M, KS * 128], scale bytes [M, KS]), by the layout's definition."""
-    KS, Mp = -(-K // 128), -(-M // 8) * 8
-    KW = -(-KS // 4)
-    raw = ws.cpu().numpy()
-    c = raw[:KS * Mp * 128].reshape(KS, Mp, 8, 16)[:, :M]
-    m = np.arange(M)[:, None]
-    chunk = np.arange(8)[None, :] ^ (m % 8)
-    codes = np.stack([c[s][m, chunk] for s in range(KS)], 1).reshape(M, KS * 128)
-    w = raw[KS * Mp * 128:].reshape(KW, Mp, 4)[:, :M]
-    return codes, w.transpose(1, 0, 2).reshape(M, KW * 4)[:, :KS]
-
-
-@pytest.mark.parametrize("M,K,ldx", [(1, 8, 8), (3, 136, 136), (9, 512, 520), (37, 640, 648), (130, 1032, 1032),
-                                     (2, 4104, 4112), (3000, 264, 264)])
+@pytest.mark.parametrize("M,K,ldx", [(1, 8, 8), (3, 136, 136), (9, 512, 520), (37, 640, 648), (64, 264, 264),
+                                     (130, 1032, 1032), (128, 1032, 1040), (2, 4104, 4112), (3000, 264, 264)])
 def test_quantizer_bit_for_bit(M, K, ldx):
+    """Against the identity the layer returns q(X) itself: a code's 4 bits fit bf16, and the identity's codes are
+    exact."""
     x = rand(M + K, M, K) * np.exp2(np.random.default_rng(1).integers(-20, 20, size=(M, 1)).astype(float))
     x[0, :min(K, 128)] = 0
     if M > 2:
-        x[1, 0], x[1, 1] = 2.0 ** -133, -2.0 ** -127           # subnormals and the smallest scale
-        x[2, 0], x[2, 1], x[2, -1] = 3.3e38, -1e30, 448
+        x[1, 0], x[1, 1] = 2.0 ** -110, -2.0 ** -112            # a block far below the others
+        x[2, 0], x[2, 1], x[2, -1] = 3e38, -1e30, 448
     if M > 8:
-        x[5, 3], x[6, 4], x[7, 130 % K] = np.inf, np.nan, -np.inf
         x[8, 0], x[8, 1] = 448, 0.875                           # a maximum that is just 448 * 2^0
-    t = torch.zeros(M, ldx, dtype=torch.bfloat16)
+    t = torch.full((M, ldx), 7.0, dtype=torch.bfloat16)
     t[:, :K] = bf16(x)
-    ws = G.poisoned_u8(lib.fp8_workspace_size(M, K))
-    lib.fp8_quantize_act(t.to(G.DEV)[:, :K], ws)
+    Y = layer.FP8Linear(torch.eye(K, dtype=torch.bfloat16, device=G.DEV))(t.to(G.DEV)[:, :K])
     G.check_ok()
-    codes, bytes_ = unpack(ws, M, K)
-    v, e = fp8.quantize(bf16(x).double().numpy())
-    assert np.array_equal(bytes_.astype(int) - 127, e)
-    want = fp8.encode(v).reshape(M, -1)
-    nan = np.isnan(v).reshape(M, -1)
-    assert np.array_equal(codes[~nan], want[~nan]) and (codes[nan] & 127 == 127).all()
+    want = fp8.value(bf16(x).double().numpy())
+    assert np.array_equal(G.bf16_host(Y), want)
+
+
+def test_smallest_magnitudes():
+    """Subnormal inputs under the smallest scale: the code's value, or zero where the tensor core flushes a
+    subnormal sum."""
+    x = np.zeros((4, 128))
+    x[0, 0], x[1, 1], x[2, 2], x[3, 3] = 2.0 ** -133, 3 * 2.0 ** -130, -2.0 ** -127, 2.0 ** -126
+    Y = G.bf16_host(layer.FP8Linear(torch.eye(128, dtype=torch.bfloat16, device=G.DEV))(bf16(x).to(G.DEV)))
+    want = fp8.value(x)
+    assert ((Y == want) | ((Y == 0) & (np.abs(want) < 2.0 ** -126))).all() and Y[3, 3] == 2.0 ** -126
 
 
 def run_linear(x, w, b, epilogue=0, begin=0, ldx=None, ldy=None):
