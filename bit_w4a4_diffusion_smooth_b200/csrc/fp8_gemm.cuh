@@ -25,7 +25,7 @@ struct Params {
   const uint8_t *x;             // their codes [KS][Mp][128] and
   const uint32_t *sx;           // scale words [KW][Mp] (many rows only)
   const uint8_t *w;             // weight codes [experts][KS][N][128]
-  const uint32_t *sw;           // weight scale words [experts][KW][N]
+  const uint32_t *sw;           // weight scale atoms [experts][ceil(N / 128)][KW][128 words]
   const uint16_t *bias;         // [experts][N] bf16 or null
   uint16_t *Y;
   size_t ldy;
@@ -57,6 +57,9 @@ __device__ __forceinline__ bool elect_one() {
   return pred != 0;
 }
 
+// Operand descriptors as a 64-bit value to add to: `bytes` further on in shared memory, inside its 256 KB.
+__host__ __device__ constexpr uint64_t desc_step(int bytes) { return static_cast<uint64_t>(bytes >> 4); }
+
 // Instruction descriptor: A and B e4m3 (0), ue8m0 scales (bit 23), N >> 3 at 17, M >> 4 at 24, K-major.
 __host__ __device__ constexpr uint32_t idesc_mxf8(int m, int n) {
   return (1u << 23) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
@@ -64,6 +67,11 @@ __host__ __device__ constexpr uint32_t idesc_mxf8(int m, int n) {
 // ... with byte `a` of A's scale words (bit 29) and byte `b` of B's (bit 4).
 __device__ __forceinline__ uint32_t with_scale_bytes(uint32_t idesc, uint32_t a, uint32_t b) {
   return idesc | (b << 4) | (a << 29);
+}
+
+// The weights' scale atom kw of the 128 columns of tile `tile128`.
+__device__ __forceinline__ const uint32_t *weight_atom(const Params &p, int expert, int tile128, int kw) {
+  return p.sw + ((static_cast<size_t>(expert) * ((p.N + 127) / 128) + tile128) * p.KW + kw) * (kScaleAtom / 4);
 }
 
 __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {

@@ -12,14 +12,15 @@
 // against 14), and the quantizer runs once in front.
 //
 // Roles (one CTA per SM, persistent over units of work):
-//   warp 0     producer: per k-stage 128 weight rows (and, quantized before,
-//              the rows of X) of 128 bytes, one bulk copy each (both are
-//              stored as their shared-memory images)
-//   warp 1     owns TMEM; one thread copies scale words into TMEM (tcgen05.cp,
-//              every fourth stage; FUSED: the activations' every stage) and
-//              issues the MMAs
-//   warp 2     brings the scale words of the next four stages into shared
-//              memory in the copy's layout
+//   warp 0     producer: per stage of two blocks of 128 along K, 128 weight
+//              rows of each, their scale atom and (quantized before) the rows
+//              of X, by bulk copies: all are stored as their shared-memory
+//              images.  The atom covers four blocks and comes with every two
+//              (1.5% more from L2)
+//   warp 1     owns TMEM; one thread copies scale words into TMEM (tcgen05.cp)
+//              and issues the MMAs
+//   warp 2     quantized before: brings the activations' scale words of the
+//              next four blocks into shared memory in the copy's layout
 //   warps 4-7  epilogue: drain the accumulator (two of them in TMEM, so the
 //              next unit's MMAs run meanwhile), bias, GELU, bf16, and turn
 //              the tile through shared memory into 16-byte row segments
@@ -30,6 +31,9 @@
 // Few units of work leave SMs idle; then clusters of 2, 4 or 8 CTAs split K,
 // and add their accumulators in a fixed order through distributed shared
 // memory (no workspace, no atomics, the same bits every time).
+// Two blocks a stage halve what the MMA thread spends between MMAs (a wait, a
+// commit, the loop: 350 cycles), which had set the pace: a weight stream of
+// 16 KB per 540 cycles and SM.
 // Every wait is bounded; one that runs out records SVDQ_ERR_TIMEOUT, raises
 // the abort flag, and the CTA drains its copies and MMAs, frees TMEM and ends.
 #include <cuda_runtime.h>
@@ -44,9 +48,10 @@ namespace fp8 {
 namespace {
 
 constexpr int TILE_N = 128;                    // output columns per unit
-constexpr int W_BYTES = TILE_N * kBlock;
+constexpr int W_BLOCK = TILE_N * kBlock;
+constexpr int W_BYTES = 2 * W_BLOCK;           // a stage: two blocks of 128 along K
 constexpr int EPI_WARPS = 4;
-constexpr int SF_BUFS = 4;                     // weight scale words of 4 x 4 k-stages
+constexpr int SF_BUFS = 4;                     // not FUSED: the activations' scale words of 4 x 4 blocks
 constexpr int EPI_STAGE = 32 * 64;             // a warp's 32 rows x 32 columns of bf16
 
 template <int TOK>
@@ -54,33 +59,56 @@ struct Shape {
   static constexpr bool FUSED = few_fused(TOK);
   static constexpr int ALIGN = FUSED ? 1 : 8;             // first rows of token tiles
   static constexpr int XW = FUSED ? 8 : 0;                // quantizing warps
-  static constexpr int XG = TOK / 16;                     // ... that share a stage, 16 rows each
+  static constexpr int XG = 2;                            // ... that share a stage, a block each
   static constexpr int TURNS = XW / XG;                   // stages in work at once
+  static constexpr int X_BLOCK = TOK * kBlock;
   static constexpr int THREADS = (8 + XW) * 32;
-  static constexpr int STAGE = W_BYTES + TOK * kBlock;
-  // as many stages as 196 KB holds: each has 16 KB of weights in flight
+  static constexpr int STAGE = W_BYTES + 2 * X_BLOCK;
+  // as many stages as 196 KB holds: each has 32 KB of weights in flight
   static constexpr int STAGES = (196 * 1024) / STAGE;
   static constexpr int SFX_BUFS = FUSED ? STAGES : SF_BUFS;   // the activations' scale atoms: per stage if FUSED
   static constexpr int SFX_OFF = STAGES * STAGE;
-  static constexpr int SFW_OFF = SFX_OFF + SFX_BUFS * kScaleAtom;
-  static constexpr int EPI_OFF = SFW_OFF + SF_BUFS * kScaleAtom;
+  static constexpr int SFW_OFF = SFX_OFF + SFX_BUFS * kScaleAtom;   // the weights' scale atoms, per stage
+  static constexpr int EPI_OFF = SFW_OFF + STAGES * kScaleAtom;
   static constexpr int TAB_OFF = EPI_OFF + EPI_WARPS * EPI_STAGE;
   static constexpr int BAR_OFF = (TAB_OFF + static_cast<int>(sizeof(ExpertTable)) + 15) & ~15;
   static constexpr int BYTES = 1024 + BAR_OFF + 512;
   static constexpr uint32_t SFX_COL = 2 * TOK;            // behind the two accumulators
   static constexpr uint32_t SFW_COL = SFX_COL + 4 * SFX_BUFS;
-  static constexpr uint32_t TMEM_COLS = SFW_COL + 4 * SF_BUFS <= 128 ? 128 : TOK <= 64 ? 256 : 512;
+  static constexpr uint32_t TMEM_COLS = SFW_COL + 4 * STAGES <= 128 ? 128 : TOK <= 64 ? 256 : 512;
+  static_assert(!FUSED || TOK == 16, "a quantizing warp takes 16 rows of a block");
   static_assert(STAGE % 1024 == 0, "operand tiles start on 1024-byte boundaries");
-  static_assert(SFW_COL + 4 * SF_BUFS <= TMEM_COLS, "accumulators and scales fit in TMEM");
+  static_assert(SFW_COL + 4 * STAGES <= TMEM_COLS, "accumulators and scales fit in TMEM");
   static_assert(TOK * TILE_N * 4 <= SFX_OFF, "a split's partial sums fit over the stages");
   static_assert(BYTES <= 232448, "fits in shared memory");
 };
 
-// A place in a CTA's sequence of k-stages: its unit of work and the stage in it.
+__device__ __forceinline__ void st_cluster_v2(uint32_t cluster_addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(cluster_addr), "r"(a), "r"(b) : "memory");
+}
+
+// A place in a CTA's sequence of stages: its unit of work and the stage in it.
 struct Cursor {
-  int item, ks;
+  int item, kp;
   Item u;
 };
+
+// Asks for the weights of this CTA's first stages in L2 while the kernel in front still runs: a hint without
+// effect on what later loads return, so it may run ahead of the wait.  For a dense call, whose first unit's
+// column tile does not depend on the table.
+__device__ __forceinline__ void prefetch_weights(const Params &p, int split, int stages) {
+  const int rank = static_cast<int>(blockIdx.x) % split, nt = static_cast<int>(blockIdx.x) / split;
+  const int cols = min(TILE_N, p.N - nt * TILE_N);
+  const int pairs = (p.KS + 1) / 2;
+  const int ks0 = 2 * (pairs * rank / split), ks1 = min(min(2 * (pairs * (rank + 1) / split), ks0 + 2 * stages), p.KS);
+  const int ks = ks0 + static_cast<int>(threadIdx.x);
+  if (cols > 0 && ks < ks1)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.w + (static_cast<size_t>(ks) * p.N +
+                                                                           static_cast<size_t>(nt) * TILE_N) *
+                                                                              kBlock),
+                 "r"(cols * kBlock)
+                 : "memory");
+}
 
 template <int TOK, int EPI>
 __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1)
@@ -124,7 +152,10 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1)
   // FUSED: nothing is read before the kernel in front has completed.  Otherwise that kernel is the quantizer,
   // which lets this one start only after its own wait: everything older (offsets and weights among it) has
   // completed by now, and only X's codes and scales have to be waited for, where they are first read.
-  if constexpr (S::FUSED) dev::grid_dependency_wait();
+  if constexpr (S::FUSED) {
+    if (p.offsets == nullptr && warp == 0) prefetch_weights(p, split, S::STAGES);
+    dev::grid_dependency_wait();
+  }
   dev::grid_launch_dependents();
   if (warp == 2) fill_expert_table(p, TOK, S::ALIGN, tab);
   dev::tc_fence_before();
@@ -136,26 +167,32 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1)
   // this CTA's share of K: its rank in the cluster of `split` CTAs that share a unit
   const int rank = static_cast<int>(blockIdx.x) % split;
   const int first_item = static_cast<int>(blockIdx.x) / split, stride = static_cast<int>(gridDim.x) / split;
-  const int ks0 = p.KS * rank / split, ks1 = p.KS * (rank + 1) / split;
+  const int pairs = (p.KS + 1) / 2;                       // stages of the whole K
+  const int kp0 = pairs * rank / split, kp1 = pairs * (rank + 1) / split;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (elect_one()) {
-      // a stage's weights; its rows of X come with them or behind them
-      const auto load_weights = [&](const Item &u, int ks, int s) {
-        // rows past the end of a buffer are not copied: what the stage holds there reaches no output
+      // a stage's weights and their scales; its rows of X come with them or behind them.  Rows past the end of a
+      // buffer are not copied: what the stage holds there reaches no output.
+      const auto load_weights = [&](const Item &u, int kp, int s) {
         const uint32_t wbytes = static_cast<uint32_t>(min(TILE_N, p.N - u.nt * TILE_N)) * kBlock;
         const uint32_t xbytes = S::FUSED ? 0u : static_cast<uint32_t>(min(TOK, p.Mp - u.row0)) * kBlock;
-        dev::mbar_arrive_expect_tx(&full[s], wbytes + xbytes);
-        dev::bulk_load(smem + s * S::STAGE,
-                       p.w + ((static_cast<size_t>(u.expert) * p.KS + ks) * p.N + static_cast<size_t>(u.nt) * TILE_N) * kBlock,
-                       wbytes, &full[s]);
+        const int blocks = min(2, p.KS - 2 * kp);
+        dev::mbar_arrive_expect_tx(&full[s], blocks * (wbytes + xbytes) + kScaleAtom);
+        for (int b = 0; b < blocks; ++b)
+          dev::bulk_load(smem + s * S::STAGE + b * W_BLOCK,
+                         p.w + ((static_cast<size_t>(u.expert) * p.KS + 2 * kp + b) * p.N +
+                                static_cast<size_t>(u.nt) * TILE_N) *
+                                   kBlock,
+                         wbytes, &full[s]);
+        dev::bulk_load(smem + S::SFW_OFF + s * kScaleAtom, weight_atom(p, u.expert, u.nt, kp >> 1), kScaleAtom, &full[s]);
       };
       int ahead = 0;                                      // stages whose weights are under way before X is there
       if constexpr (!S::FUSED) {
         if (first_item < items) {
           const Item u = find_item(p, tab, TOK, S::ALIGN, ntn, first_item);
-          for (; ahead < min(S::STAGES, ks1 - ks0); ++ahead) load_weights(u, ks0 + ahead, ahead);
+          for (; ahead < min(S::STAGES, kp1 - kp0); ++ahead) load_weights(u, kp0 + ahead, ahead);
         }
         dev::grid_dependency_wait();
       }
@@ -163,18 +200,21 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1)
       bool ok = true;
       for (int item = first_item; item < items && ok; item += stride) {
         const Item u = find_item(p, tab, TOK, S::ALIGN, ntn, item);
-        for (int ks = ks0; ks < ks1; ++ks, ++it) {
+        for (int kp = kp0; kp < kp1; ++kp, ++it) {
           const int s = it % S::STAGES;
           if (it >= ahead) {
             if (!dev::mbar_wait(&empty[s], ((it / S::STAGES) & 1) ^ 1, p.limit_ns, abort_flag)) {
               ok = false;
               break;
             }
-            load_weights(u, ks, s);
+            load_weights(u, kp, s);
           }
-          if constexpr (!S::FUSED)
-            dev::bulk_load(smem + s * S::STAGE + W_BYTES, p.x + (static_cast<size_t>(ks) * p.Mp + u.row0) * kBlock,
-                           static_cast<uint32_t>(min(TOK, p.Mp - u.row0)) * kBlock, &full[s]);
+          if constexpr (!S::FUSED) {
+            for (int b = 0; b < min(2, p.KS - 2 * kp); ++b)
+              dev::bulk_load(smem + s * S::STAGE + W_BYTES + b * S::X_BLOCK,
+                             p.x + (static_cast<size_t>(2 * kp + b) * p.Mp + u.row0) * kBlock,
+                             static_cast<uint32_t>(min(TOK, p.Mp - u.row0)) * kBlock, &full[s]);
+          }
         }
       }
       if (!ok) {
@@ -190,6 +230,8 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1)
     // ------------------------------------------------------------ scales into TMEM, MMAs
     if (elect_one()) {
       constexpr uint32_t idesc = idesc_mxf8(TILE_N, TOK);
+      const uint32_t base = dev::smem_u32(smem);
+      const uint64_t desc0 = dev::desc_sw128(base), sfw0 = dev::desc_sf(base + S::SFW_OFF), sfx0 = dev::desc_sf(base + S::SFX_OFF);
       int it = 0, quad = 0, n = 0;
       bool ok = true, issued = false;
       for (int item = first_item; item < items && ok; item += stride, ++n) {
@@ -200,35 +242,44 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1)
         }
         dev::tc_fence_after();
         const uint32_t acc = tmem + a * TOK;
-        for (int ks = ks0; ks < ks1; ++ks, ++it) {
+        uint32_t accumulate = 0;
+        for (int kp = kp0; kp < kp1; ++kp, ++it) {
           const int s = it % S::STAGES, b = quad % SF_BUFS;
-          const uint32_t sfw = tmem + S::SFW_COL + 4 * b, sfx = tmem + S::SFX_COL + 4 * (S::FUSED ? s : b);
-          if ((ks & 3) == 0 || ks == ks0) {
-            if (!dev::mbar_wait(&sf_full[b], (quad / SF_BUFS) & 1, p.limit_ns, abort_flag)) {
-              ok = false;
-              break;
+          const uint32_t sfw = tmem + S::SFW_COL + 4 * s, sfx = tmem + S::SFX_COL + 4 * (S::FUSED ? s : b);
+          if constexpr (!S::FUSED) {
+            if ((kp & 1) == 0 || kp == kp0) {
+              if (!dev::mbar_wait(&sf_full[b], (quad / SF_BUFS) & 1, p.limit_ns, abort_flag)) {
+                ok = false;
+                break;
+              }
+              dev::tc_fence_after();
+              dev::tmem_cp_32x128b_x4(sfx, sfx0 + desc_step(kScaleAtom) * b);
+              issued = true;
             }
-            dev::tc_fence_after();
-            dev::tmem_cp_32x128b_x4(sfw, dev::desc_sf(dev::smem_u32(smem + S::SFW_OFF + b * kScaleAtom)));
-            if constexpr (!S::FUSED)
-              dev::tmem_cp_32x128b_x4(sfx, dev::desc_sf(dev::smem_u32(smem + S::SFX_OFF + b * kScaleAtom)));
-            issued = true;
           }
           if (!dev::mbar_wait(&full[s], (it / S::STAGES) & 1, p.limit_ns, abort_flag)) {
             ok = false;
             break;
           }
           dev::tc_fence_after();
-          if constexpr (S::FUSED)
-            dev::tmem_cp_32x128b_x4(sfx, dev::desc_sf(dev::smem_u32(smem + S::SFX_OFF + s * kScaleAtom)));
-          const uint32_t sw = dev::smem_u32(smem + s * S::STAGE), sx = sw + W_BYTES;
-          const uint32_t id = with_scale_bytes(idesc, ks & 3, S::FUSED ? 0 : ks & 3);
+          issued = true;
+          dev::tmem_cp_32x128b_x4(sfw, sfw0 + desc_step(kScaleAtom) * s);
+          if constexpr (S::FUSED) dev::tmem_cp_32x128b_x4(sfx, sfx0 + desc_step(kScaleAtom) * s);
+          const uint64_t dw = desc0 + desc_step(S::STAGE) * s;
 #pragma unroll
-          for (int j = 0; j < 4; ++j)                     // K = 32 codes = 32 bytes per MMA
-            umma_mxf8(acc, dev::desc_sw128(sw + 32 * j), dev::desc_sw128(sx + 32 * j), id, sfw, sfx,
-                      ks > ks0 || j > 0 ? 1u : 0u);
+          for (int blk = 0; blk < 2; ++blk) {
+            if (2 * kp + blk >= p.KS) break;
+            const uint32_t w_byte = 2 * (kp & 1) + blk;   // of a word of four blocks
+            const uint32_t id = with_scale_bytes(idesc, w_byte, S::FUSED ? blk : w_byte);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {                 // K = 32 codes = 32 bytes per MMA
+              umma_mxf8(acc, dw + desc_step(blk * W_BLOCK + 32 * j), dw + desc_step(W_BYTES + blk * S::X_BLOCK + 32 * j),
+                        id, sfw, sfx, accumulate);
+              accumulate = 1;
+            }
+          }
           dev::tc_commit(&empty[s]);
-          if ((ks & 3) == 3 || ks == ks1 - 1) {
+          if (!S::FUSED && ((kp & 1) == 1 || kp == kp1 - 1)) {
             dev::tc_commit(&sf_empty[b]);
             ++quad;
           }
@@ -245,37 +296,26 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1)
         dev::mbar_wait(drain, 0, p.limit_ns, nullptr);
       }
     }
-  } else if (warp == 2) {
-    // ------------------------------------------------------------ scale words
-    if constexpr (!S::FUSED) dev::grid_dependency_wait();
+  } else if (!S::FUSED && warp == 2) {
+    // ------------------------------------------------------------ the activations' scale words
+    dev::grid_dependency_wait();
     int quad = 0;
     bool ok = true;
     for (int item = first_item; item < items && ok; item += stride) {
       const Item u = find_item(p, tab, TOK, S::ALIGN, ntn, item);
-      for (int kw = ks0 >> 2; 4 * kw < ks1; ++kw, ++quad) {
+      for (int kw = kp0 >> 1; 2 * kw < kp1; ++kw, ++quad) {
         const int b = quad % SF_BUFS;
-        const uint32_t *ws = p.sw + (static_cast<size_t>(u.expert) * p.KW + kw) * p.N;
-        uint32_t ww[4];
+        uint32_t xw[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int col = u.nt * TILE_N + 32 * i + lane;
-          ww[i] = col < p.N ? __ldg(ws + col) : 0u;
-        }
-        uint32_t xw[4];
-        if constexpr (!S::FUSED) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = u.row0 + 32 * i + lane;
-            xw[i] = 32 * i + lane < TOK && row < p.Mp ? p.sx[static_cast<size_t>(kw) * p.Mp + row] : 0u;
-          }
+          const int row = u.row0 + 32 * i + lane;
+          xw[i] = 32 * i + lane < TOK && row < p.Mp ? p.sx[static_cast<size_t>(kw) * p.Mp + row] : 0u;
         }
         if (!dev::mbar_wait_warp(&sf_empty[b], ((quad / SF_BUFS) & 1) ^ 1, p.limit_ns, abort_flag)) {
           ok = false;
           break;
         }
-        reinterpret_cast<uint4 *>(smem + S::SFW_OFF + b * kScaleAtom)[lane] = make_uint4(ww[0], ww[1], ww[2], ww[3]);
-        if constexpr (!S::FUSED)
-          reinterpret_cast<uint4 *>(smem + S::SFX_OFF + b * kScaleAtom)[lane] = make_uint4(xw[0], xw[1], xw[2], xw[3]);
+        reinterpret_cast<uint4 *>(smem + S::SFX_OFF + b * kScaleAtom)[lane] = make_uint4(xw[0], xw[1], xw[2], xw[3]);
         dev::fence_proxy_async();
         __syncwarp();
         if (lane == 0) dev::mbar_arrive(&sf_full[b]);
@@ -289,12 +329,12 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1)
   if constexpr (S::FUSED) {
     if (warp >= 8) {
       // ---------------------------------------------------------- quantize X
-      const int xw = (warp - 8) % S::XG, turn = (warp - 8) / S::XG, sub = lane >> 3, chunk = lane & 7;
-      uint32_t raw[4][8];
+      const int blk = (warp - 8) % S::XG, turn = (warp - 8) / S::XG, sub = lane >> 3, chunk = lane & 7;
+      uint32_t raw[4][8];                                 // 16 rows of a block, 4 at a time
       const auto load = [&](const Cursor &c) {
 #pragma unroll
         for (int st = 0; st < 4; ++st) {
-          const int row = c.u.row0 + 4 * (xw + S::XG * st) + sub, k = c.ks * kBlock + chunk * 16;
+          const int row = c.u.row0 + 4 * st + sub, k = (2 * c.kp + blk) * kBlock + chunk * 16;
           const uint4 *src = reinterpret_cast<const uint4 *>(p.X + static_cast<size_t>(row) * p.ldx + k);
           const bool live = row < c.u.end;
           const uint4 v0 = live && k < p.K ? __ldg(src) : make_uint4(0, 0, 0, 0);
@@ -306,11 +346,11 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1)
       // `stages` stages on in the CTA's sequence
       const auto advance = [&](Cursor &c, int stages) {
         const int item = c.item;
-        for (c.ks += stages; c.ks >= ks1; c.ks -= ks1 - ks0) c.item += stride;
+        for (c.kp += stages; c.kp >= kp1; c.kp -= kp1 - kp0) c.item += stride;
         if (c.item != item && c.item < items) c.u = find_item(p, tab, TOK, S::ALIGN, ntn, c.item);
       };
       bool ok = true;
-      Cursor c{first_item, ks0, {}};
+      Cursor c{first_item, kp0, {}};
       if (first_item < items) {
         c.u = find_item(p, tab, TOK, S::ALIGN, ntn, first_item);
         advance(c, turn);
@@ -318,12 +358,12 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1)
       }
       for (int it = turn; c.item < items; it += S::TURNS) {
         const int s = it % S::STAGES;
-        uint8_t *dst = smem + s * S::STAGE + W_BYTES, *sfx = smem + S::SFX_OFF + s * kScaleAtom;
+        uint8_t *dst = smem + s * S::STAGE + W_BYTES + blk * S::X_BLOCK, *sfx = smem + S::SFX_OFF + s * kScaleAtom + blk;
         uint32_t code[4][4], byte[4];
-        const int rows = c.u.end - c.u.row0 - 4 * xw;     // step st has rows if 4 XG st is below this
+        const int rows = 2 * c.kp + blk < p.KS ? c.u.end - c.u.row0 : 0;   // step st has rows if 4 st is below this
 #pragma unroll
         for (int st = 0; st < 4; ++st)
-          if (4 * S::XG * st < rows) byte[st] = quantize16(raw[st], code[st]);
+          if (4 * st < rows) byte[st] = quantize16(raw[st], code[st]);
         advance(c, S::TURNS);
         if (c.item < items) load(c);
         if (!dev::mbar_wait_warp(&empty[s], ((it / S::STAGES) & 1) ^ 1, p.limit_ns, abort_flag)) {
@@ -332,11 +372,11 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1)
         }
 #pragma unroll
         for (int st = 0; st < 4; ++st) {
-          if (4 * S::XG * st >= rows) break;
-          const int r = 4 * (xw + S::XG * st) + sub;      // rows past the expert's: zeros, which reach no output
+          if (4 * st >= rows) break;
+          const int r = 4 * st + sub;                     // rows past the expert's: zeros, which reach no output
           *reinterpret_cast<uint4 *>(dst + r * kBlock + ((chunk ^ (r & 7)) << 4)) =
               make_uint4(code[st][0], code[st][1], code[st][2], code[st][3]);
-          if (chunk == 0) *reinterpret_cast<uint32_t *>(sfx + (r & 31) * 16 + (r >> 5) * 4) = byte[st];
+          if (chunk == 0) sfx[r * 16] = static_cast<uint8_t>(byte[st]);
         }
         dev::fence_proxy_async();
         __syncwarp();
@@ -420,7 +460,8 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1)
     }
   } else {
     // One unit per cluster.  CTA j of the cluster finishes rows [j TC, (j + 1) TC) of the tile; the others send
-    // it their sums of those rows: [rank][row][column] floats over its (idle) stages.
+    // it their sums of those rows, over its (idle) stages: [rank][two rows][column][2] floats, 8 bytes a lane, so
+    // a warp's store or load is 256 contiguous bytes.
     const int TC = TOK / split;
     const bool mine = first_item < items;
     const Item u = mine ? find_item(p, tab, TOK, S::ALIGN, ntn, first_item) : Item{};
@@ -434,38 +475,45 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1)
     }
     __syncwarp();
     dev::cluster_sync();                                  // every CTA of the cluster is done with its stages
+    const int col = u.nt * TILE_N + 32 * q + lane;
     if (ok) {
       dev::tc_fence_after();
-      const uint32_t base = dev::smem_u32(smem) + static_cast<uint32_t>(rank * TC * TILE_N + 32 * q + lane) * 4u;
+      const uint32_t base = dev::smem_u32(smem) + static_cast<uint32_t>(rank * TC * TILE_N + 64 * q + 2 * lane) * 4u;
 #pragma unroll 1
       for (int c = 0; c < TOK && u.row0 + c < u.end; c += CH) {
         uint32_t v[CH];
         read_chunk(0, c, v);
 #pragma unroll
-        for (int t = 0; t < CH; ++t) {
+        for (int t = 0; t < CH; t += 2) {
           const int j = (c + t) / TC;
-          dev::st_cluster_u32(dev::mapa(base + static_cast<uint32_t>((c + t - j * TC) * TILE_N) * 4u, j), v[t]);
+          st_cluster_v2(dev::mapa(base + static_cast<uint32_t>((c + t - j * TC) * TILE_N) * 4u, j), v[t], v[t + 1]);
         }
       }
     }
     __syncwarp();
     dev::cluster_sync();                                  // all sums have arrived
     if (ok) {
-      const int row0 = u.row0 + rank * TC, col = u.nt * TILE_N + 32 * q + lane;
+      const int row0 = u.row0 + rank * TC;
       const float bias = bias_of(u, col);
-      const float *part = reinterpret_cast<const float *>(smem) + 32 * q + lane;
+      const float2 *part = reinterpret_cast<const float2 *>(smem) + 32 * q + lane;
 #pragma unroll 1
-      for (int c = 0; c < TC && row0 + c < u.end; c += 32) {
-        const int rows = min(32, TC - c);
-#pragma unroll 1
-        for (int t = 0; t < rows; t += 2) {
-          float y0 = 0.0f, y1 = 0.0f;
-          for (int j = 0; j < split; ++j) {               // in the order of K
-            y0 += part[(j * TC + c + t) * TILE_N];
-            y1 += part[(j * TC + c + t + 1) * TILE_N];
-          }
-          finish2(y0, y1, bias, col >= p.gelu_col_begin, t);
+      for (int c = 0; c < TC && row0 + c < u.end; c += 16) {
+        const int rows = min(16, TC - c);
+        float2 y[8];
+#pragma unroll
+        for (int t = 0; t < 8; ++t) y[t] = make_float2(0.0f, 0.0f);
+        for (int j = 0; j < split; ++j) {                 // in the order of K
+#pragma unroll
+          for (int t = 0; t < 8; ++t)
+            if (2 * t < rows) {
+              const float2 f = part[(j * TC + c + 2 * t) / 2 * TILE_N];
+              y[t].x += f.x;
+              y[t].y += f.y;
+            }
         }
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+          if (2 * t < rows) finish2(y[t].x, y[t].y, bias, col >= p.gelu_col_begin, 2 * t);
         store(u, row0 + c, rows);
       }
     }

@@ -290,7 +290,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const Item u = find_item(p, tab, TOK, 8, ntn, item);
       for (int kw = 0; kw < p.KW; ++kw, ++quad) {
         const int b = quad % SF_BUFS;
-        const uint32_t *ws = p.sw + (static_cast<size_t>(u.expert) * p.KW + kw) * p.N;
         const uint32_t *xs = p.sx + static_cast<size_t>(kw) * p.Mp;
         uint32_t xw[4], ww[8];
 #pragma unroll
@@ -301,7 +300,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int r = 32 * i + lane, col = u.nt * TILE_N + r;
-          ww[i] = r < TILE_N && col < p.N ? __ldg(ws + col) : 0u;
+          ww[i] = r < TILE_N && col < p.N
+                      ? __ldg(weight_atom(p, u.expert, col >> 7, kw) + (col & 31) * 4 + ((col >> 5) & 3))
+                      : 0u;
         }
         const bool got = dev::mbar_wait_cluster(&sf_empty[b], ((quad / SF_BUFS) & 1) ^ 1, p.limit_ns, abort_flag);
         if (!__all_sync(0xFFFFFFFFu, got)) {

@@ -16,9 +16,12 @@
 //   activations  codes  [KS][Mp][128], Mp = M rounded up to 8
 //                scales [KW][Mp] words
 //   weights      codes  [experts][KS][N][128]   (N % 8 == 0)
-//                scales [experts][KW][N] words
-// Codes past K are zero in both; activation rows past M are never written and
-// never reach an output.
+//                scales [experts][NT][KW][512 bytes], NT = ceil(N / 128): an
+//                       atom holds the words of 128 columns as a tcgen05.cp
+//                       32x128b.warpx4 copy reads them, column c's word at
+//                       (c % 32) * 16 + (c / 32) * 4
+// Codes past K are zero in both; activation rows past M and words of columns
+// past N are never written and never reach an output.
 #pragma once
 
 #include <cstddef>
@@ -28,7 +31,7 @@ namespace svdq {
 namespace fp8 {
 
 constexpr int kBlock = 128;
-constexpr int kScaleAtom = 512;      // scale words of 128 rows as a tcgen05.cp 32x128b.warpx4 copy reads them
+constexpr int kScaleAtom = 512;
 
 inline int k_stages(int K) { return (K + kBlock - 1) / kBlock; }
 inline int k_words(int K) { return (k_stages(K) + 3) / 4; }
@@ -54,7 +57,7 @@ inline size_t weight_code_bytes(int K, int N, int experts) {
 }
 inline size_t weight_bytes(int K, int N, int experts) {
   return weight_code_bytes(K, N, experts) +
-         static_cast<size_t>(experts) * static_cast<size_t>(k_words(K)) * static_cast<size_t>(N) * 4u;
+         static_cast<size_t>(experts) * static_cast<size_t>((N + 127) / 128) * static_cast<size_t>(k_words(K)) * kScaleAtom;
 }
 
 }  // namespace fp8

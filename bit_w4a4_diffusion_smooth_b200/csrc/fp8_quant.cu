@@ -89,7 +89,8 @@ __global__ void __launch_bounds__(PACK_COLS)
     }
     *reinterpret_cast<uint4 *>(dst + ((c ^ (n & 7)) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
   }
-  uint8_t *word = scales + ((static_cast<size_t>(e) * KW + ks / 4) * N + n) * 4;
+  uint8_t *word = scales + ((static_cast<size_t>(e) * gridDim.y + blockIdx.y) * KW + ks / 4) * kScaleAtom +
+                  (threadIdx.x & 31) * 16 + (threadIdx.x >> 5) * 4;
   word[ks & 3] = static_cast<uint8_t>(byte);
   if (ks == KS - 1)                              // the blocks past K of the last word
     for (int j = (ks & 3) + 1; j < 4; ++j) word[j] = 127;
