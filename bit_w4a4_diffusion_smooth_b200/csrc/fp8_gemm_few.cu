@@ -79,7 +79,7 @@ struct Shape {
   static_assert(!FUSED || TOK == 16, "a quantizing warp takes 16 rows of a block");
   static_assert(STAGE % 1024 == 0, "operand tiles start on 1024-byte boundaries");
   static_assert(SFW_COL + 4 * STAGES <= TMEM_COLS, "accumulators and scales fit in TMEM");
-  static_assert(TOK * TILE_N * 4 <= SFX_OFF, "a split's partial sums fit over the stages");
+  static_assert(TOK * TILE_N * 4 + 4 * EPI_STAGE <= SFX_OFF, "a split's sums and staging fit over the stages");
   static_assert(BYTES <= 232448, "fits in shared memory");
 };
 
@@ -159,6 +159,7 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1)
   dev::grid_launch_dependents();
   if (warp == 2) fill_expert_table(p, TOK, S::ALIGN, tab);
   dev::tc_fence_before();
+  __syncwarp();
   __syncthreads();
   dev::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -461,11 +462,16 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1)
   } else {
     // One unit per cluster.  CTA j of the cluster finishes rows [j TC, (j + 1) TC) of the tile; the others send
     // it their sums of those rows, over its (idle) stages: [rank][two rows][column][2] floats, 8 bytes a lane, so
-    // a warp's store or load is 256 contiguous bytes.
-    const int TC = TOK / split;
+    // a warp's store or load is 256 contiguous bytes.  The first eight warps share the rows, their roles being
+    // over.
+    const int TC = TOK / split, half = warp >> 2;
     const bool mine = first_item < items;
     const Item u = mine ? find_item(p, tab, TOK, S::ALIGN, ntn, first_item) : Item{};
-    bool ok = mine && warp >= 4 && warp < 8;
+    const int col = u.nt * TILE_N + 32 * q + lane;
+    bool ok = mine && warp < 8;
+    const float bias = ok ? bias_of(u, col) : 0.0f;       // read under the exchange
+    if (warp < 4) stage = smem + TOK * TILE_N * 4 + q * EPI_STAGE;   // behind the sums
+    __syncwarp();
     if (ok && !dev::mbar_wait_warp(&tmem_full[0], 0, p.limit_ns, abort_flag)) {
       if (lane == 0) {
         *abort_flag = 1;
@@ -475,16 +481,16 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1)
     }
     __syncwarp();
     dev::cluster_sync();                                  // every CTA of the cluster is done with its stages
-    const int col = u.nt * TILE_N + 32 * q + lane;
     if (ok) {
       dev::tc_fence_after();
       const uint32_t base = dev::smem_u32(smem) + static_cast<uint32_t>(rank * TC * TILE_N + 64 * q + 2 * lane) * 4u;
 #pragma unroll 1
-      for (int c = 0; c < TOK && u.row0 + c < u.end; c += CH) {
-        uint32_t v[CH];
-        read_chunk(0, c, v);
+      for (int c = half * 16; c < TOK && u.row0 + c < u.end; c += 32) {
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(c), v);
+        dev::tmem_wait_ld();
 #pragma unroll
-        for (int t = 0; t < CH; t += 2) {
+        for (int t = 0; t < 16; t += 2) {
           const int j = (c + t) / TC;
           st_cluster_v2(dev::mapa(base + static_cast<uint32_t>((c + t - j * TC) * TILE_N) * 4u, j), v[t], v[t + 1]);
         }
@@ -494,10 +500,9 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1)
     dev::cluster_sync();                                  // all sums have arrived
     if (ok) {
       const int row0 = u.row0 + rank * TC;
-      const float bias = bias_of(u, col);
       const float2 *part = reinterpret_cast<const float2 *>(smem) + 32 * q + lane;
 #pragma unroll 1
-      for (int c = 0; c < TC && row0 + c < u.end; c += 16) {
+      for (int c = half * 16; c < TC && row0 + c < u.end; c += 32) {
         const int rows = min(16, TC - c);
         float2 y[8];
 #pragma unroll
@@ -519,7 +524,10 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1)
     }
   }
 
+  // The elected threads' warps meet first: the 31 lanes that skipped a role would otherwise arrive at the barrier
+  // without the 32nd, count as a whole warp, and let TMEM go while other warps still read it.
   dev::tc_fence_before();
+  __syncwarp();
   __syncthreads();
   if (warp == 1) {
     dev::tc_fence_after();
