@@ -95,9 +95,32 @@ __device__ __forceinline__ float2 gelu_tanh2(float2 y) {
   return make_float2(y.x * dev::rcp_approx_ftz(1.0f + dev::ex2_approx_ftz(z.x)),
                      y.y * dev::rcp_approx_ftz(1.0f + dev::ex2_approx_ftz(z.y)));
 }
+// GELU, erf form, of two values, with one special-function instruction each: 0.5 y (1 + erf x), x = y / sqrt 2.
+// erf by Abramowitz & Stegun, Handbook of Mathematical Functions, formula 7.1.28: for x >= 0
+// 1 - erf x = (1 + a1 x + ... + a6 x^6)^-16 = q, |error| <= 3e-7; 1 + erf x is 2 - q for x >= 0 and q(|x|) below,
+// taken directly, without cancellation.  (The formula with an exponential takes two such instructions, which
+// bound the epilogue: 56 pairs a lane and half tile.)  The polynomial overflows to infinity only where q is 0.
+__device__ __forceinline__ float2 gelu_erf2_rcp(float2 y) {
+  const float2 x = dev::mul2_rn(y, make_float2(0.70710678118654752f, 0.70710678118654752f));
+  const float2 ax = make_float2(fabsf(x.x), fabsf(x.y));
+  float2 d = dev::fma2_rn(make_float2(0.0000430638f, 0.0000430638f), ax, make_float2(0.0002765672f, 0.0002765672f));
+  d = dev::fma2_rn(d, ax, make_float2(0.0001520143f, 0.0001520143f));
+  d = dev::fma2_rn(d, ax, make_float2(0.0092705272f, 0.0092705272f));
+  d = dev::fma2_rn(d, ax, make_float2(0.0422820123f, 0.0422820123f));
+  d = dev::fma2_rn(d, ax, make_float2(0.0705230784f, 0.0705230784f));
+  d = dev::fma2_rn(d, ax, make_float2(1.0f, 1.0f));
+  float2 q = make_float2(dev::rcp_approx_ftz(d.x), dev::rcp_approx_ftz(d.y));
+  q = dev::mul2_rn(q, q);
+  q = dev::mul2_rn(q, q);
+  q = dev::mul2_rn(q, q);
+  q = dev::mul2_rn(q, q);
+  const float2 r = dev::fma2_rn(make_float2(-1.0f, -1.0f), q, make_float2(2.0f, 2.0f));
+  const float2 one_plus_erf = make_float2(x.x >= 0.0f ? r.x : q.x, x.y >= 0.0f ? r.y : q.y);
+  return dev::mul2_rn(dev::mul2_rn(y, make_float2(0.5f, 0.5f)), one_plus_erf);
+}
 template <int EPI>
 __device__ __forceinline__ float2 activate2(float2 y) {
-  if constexpr (EPI == SVDQ_EPILOGUE_GELU_ERF) return dev::gelu_erf2(y);
+  if constexpr (EPI == SVDQ_EPILOGUE_GELU_ERF) return gelu_erf2_rcp(y);
   if constexpr (EPI == SVDQ_EPILOGUE_GELU_TANH) return gelu_tanh2(y);
   return y;
 }

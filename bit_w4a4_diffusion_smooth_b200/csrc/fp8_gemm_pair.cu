@@ -4,24 +4,39 @@
 // of 256 x 240 x 32: CTA h holds rows 128h..128h+127 of the token tile and
 // weight rows (output columns) 120h..120h+119, and its TMEM receives its own
 // 128 rows of the accumulator, so each SM reads 248 operand rows per k-stage
-// for 256 x 120 outputs.  (One CTA alone would read 256 for 128 x 128, and the
-// operand traffic from L2 bounds it.)  240 columns instead of 256 leave TMEM
-// room for two accumulators and the block scales: draining one (2,300 cycles a
-// tile, 12% at K = 4096) runs under the next tile's MMAs.
+// for 256 x 120 outputs.  (One CTA alone would read 256 for 128 x 128.)  240
+// columns instead of 256 leave TMEM room for two accumulators and the block
+// scales, so that a tile's epilogue runs under the next tile's MMAs.
 //
-// Roles (one CTA per SM, persistent over units of work, 12 warps):
+// What bounds it: shared memory.  A stage is written once and read once by the
+// MMAs, 2 x 248 rows x 128 bytes in the 480 cycles of its MMAs: 132 bytes a
+// cycle of the 128 an SM has, 140 with the epilogue's.  Under load the power
+// cap comes first.
+//
+// Roles (one CTA per SM, persistent over units of work, 20 warps):
 //   warp 0      producer in both CTAs: per k-stage its halves of the two
 //               operands, completing on the even CTA's `full` barrier
 //   warp 1      owns TMEM (pair allocation); in the even CTA one thread issues
-//               the MMAs and commits each stage to both CTAs
+//               the MMAs and commits each stage to both CTAs.  It has 480
+//               cycles a stage: it asks for the next stage's barrier before it
+//               issues this one's MMAs, and keeps its place in the ring by
+//               increments
 //   warp 2      scale words of the next four stages, in both CTAs: the words
 //               of its own 128 token rows and of all 240 weight rows (which
-//               both TMEMs need)
-//   warp 3      even CTA: copies them into both TMEMs (tcgen05.cp)
-//   warps 4-11  epilogue in both CTAs: 16 columns at a time from TMEM, bias,
-//               GELU, bf16; a thread holds 32 contiguous bytes of its row and
-//               stores them itself, whole sectors, so ragged ends are a
-//               condition on its row
+//               both TMEMs need).  Their loads run two sets ahead
+//   warp 3      even CTA: copies them into both TMEMs (tcgen05.cp); from the
+//               MMA thread they would stand between its MMAs
+//   warps 4-19  epilogue in both CTAs: 16 columns at a time from TMEM, bias,
+//               GELU, bf16, and 32 rows x 32 columns through shared memory to
+//               global memory, a row's 64 bytes by 4 lanes.  Sixteen warps,
+//               since GELU's chains leave a scheduler idle under two of them
+//               (10,000 cycles a tile of 9,000 of MMAs at K = 2560), and a
+//               rolled loop: unrolled over the tile the code outgrew the
+//               instruction cache
+// What crosses the pair is read by the asynchronous proxy (operands, scale
+// words) or lies in TMEM, so its barriers need no cluster-scope fence: with
+// one, an arrival waited for every load the warp had in flight, and the scale
+// words alone took 2,400 cycles a set against 1,800 of MMAs.
 // Every wait is bounded; one that runs out records SVDQ_ERR_TIMEOUT and raises
 // the abort flag of both CTAs; in-flight work is drained, the pair meets at a
 // cluster barrier and frees TMEM.
@@ -41,21 +56,24 @@ constexpr int STAGES = 6;
 constexpr int X_BYTES = 128 * kBlock;          // this CTA's token rows of a stage
 constexpr int W_BYTES = TILE_N / 2 * kBlock;   // this CTA's weight rows
 constexpr int STAGE = X_BYTES + W_BYTES;
-constexpr int SF_BUFS = 4;                     // scale words of 4 x 4 k-stages in shared memory
-constexpr int SF_TMEM = 2;                     // ... of 2 x 4 in TMEM
-constexpr int SF_BYTES = 3 * kScaleAtom;       // own token atom, the two weight atoms
-constexpr int EPI_WARPS = 8;
+constexpr int SF_BUFS = 2;                     // scale words of 2 x 4 k-stages in shared memory
+constexpr int SF_TMEM = 2;                     // ... and in TMEM
+constexpr int SF_BYTES = 3 * kScaleAtom;       // own token atom, two weight atoms
+constexpr int SF_COLS = 12;                    // token scales 4 columns, weight scales 8
+constexpr int EPI_WARPS = 16;
+constexpr int EPI_TILE = 32 * 64;              // a warp's 32 rows x 32 bf16
 constexpr int THREADS = (4 + EPI_WARPS) * 32;
 constexpr int SF_OFF = STAGES * STAGE;
-constexpr int TAB_OFF = SF_OFF + SF_BUFS * SF_BYTES;
+constexpr int EPI_OFF = SF_OFF + SF_BUFS * SF_BYTES;
+constexpr int TAB_OFF = EPI_OFF + EPI_WARPS * EPI_TILE;
 constexpr int BAR_OFF = (TAB_OFF + static_cast<int>(sizeof(ExpertTable)) + 15) & ~15;
 constexpr int SMEM_BYTES = 1024 + BAR_OFF + 256;
 constexpr uint32_t TMEM_COLS = 512;
-constexpr uint32_t SF_COL = 2 * TILE_N;        // buffer b: token scales at +12b, weight scales at +12b + 4
+constexpr uint32_t SF_COL = 2 * TILE_N;
 constexpr int MAP_ROW = 1024;                  // the operands as rows of 8 x 128 bytes
 static_assert(STAGE % 1024 == 0 && X_BYTES % 1024 == 0, "operand tiles start on 1024-byte boundaries");
 static_assert(SMEM_BYTES <= 232448, "fits in shared memory");
-static_assert(SF_COL + 12 * SF_TMEM <= TMEM_COLS, "accumulators and scales fit in TMEM");
+static_assert(SF_COL + SF_COLS * SF_TMEM <= TMEM_COLS, "accumulators and scales fit in TMEM");
 
 struct Maps {
   CUtensorMap x, w;
@@ -83,45 +101,49 @@ __device__ __forceinline__ void abort_pair(volatile int *abort_flag, uint32_t pe
   dev::report(status, SVDQ_ERR_TIMEOUT);
 }
 
-// 32 bytes to a 32-byte aligned address.
-__device__ __forceinline__ void store32(void *ptr, const uint32_t (&v)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(ptr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
-
-// Bias, activation and rounding of 16 columns from `col` on, stored to row `y` if `row_ok`; `wide`: rows of Y
-// are 32-byte aligned.
+// Bias (16 bf16), activation and rounding of 16 columns, the GELU from column `act` of the 16 on.
 template <int EPI>
-__device__ __forceinline__ void finish16(const Params &p, const uint16_t *bias, const uint32_t (&v)[16], int col,
-                                         uint16_t *y, bool row_ok, bool wide) {
-  uint32_t out[8];
+__device__ __forceinline__ void finish16(const uint32_t (&v)[16], const uint4 (&bb)[2], int act, uint32_t (&out)[8]) {
+  const uint32_t bw[8] = {bb[0].x, bb[0].y, bb[0].z, bb[0].w, bb[1].x, bb[1].y, bb[1].z, bb[1].w};
+  float2 t[8];
 #pragma unroll
-  for (int g = 0; g < 2; ++g) {
-    uint4 bb = make_uint4(0, 0, 0, 0);
-    if (bias && col + 8 * g < p.N) bb = __ldg(reinterpret_cast<const uint4 *>(bias + col + 8 * g));   // N % 8 == 0
-    const uint32_t bw[4] = {bb.x, bb.y, bb.z, bb.w};
+  for (int j = 0; j < 8; ++j)
+    t[j] = make_float2(__uint_as_float(v[2 * j]) + __uint_as_float(bw[j] << 16),
+                       __uint_as_float(v[2 * j + 1]) + __uint_as_float(bw[j] & 0xFFFF0000u));
+  if constexpr (EPI != SVDQ_EPILOGUE_NONE) {
+    if (act <= 0) {                                // the usual case, the same for all lanes
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int i = 8 * g + 2 * j;
-      const float2 t = make_float2(__uint_as_float(v[i]) + __uint_as_float(bw[j] << 16),
-                                   __uint_as_float(v[i + 1]) + __uint_as_float(bw[j] & 0xFFFF0000u));
-      float2 a = activate2<EPI>(t);
-      if constexpr (EPI != SVDQ_EPILOGUE_NONE) {
-        a.x = col + i >= p.gelu_col_begin ? a.x : t.x;
-        a.y = col + i + 1 >= p.gelu_col_begin ? a.y : t.y;
+      for (int j = 0; j < 8; ++j) t[j] = activate2<EPI>(t[j]);
+    } else if (act < 16) {
+#pragma unroll 1
+      for (int j = 0; j < 8; ++j) {
+        float2 x = t[0];                           // through the first place, so that the loop stays rolled
+        const float2 g = activate2<EPI>(x);
+        x = make_float2(2 * j >= act ? g.x : x.x, 2 * j + 1 >= act ? g.y : x.y);
+#pragma unroll
+        for (int i = 0; i < 7; ++i) t[i] = t[i + 1];
+        t[7] = x;
       }
-      const __nv_bfloat162 hv = __floats2bfloat162_rn(a.x, a.y);
-      out[4 * g + j] = *reinterpret_cast<const uint32_t *>(&hv);
     }
   }
-  if (!row_ok) return;
-  if (wide && col + 16 <= p.N) {
-    store32(y + col, out);
-  } else {
-    if (col < p.N) *reinterpret_cast<uint4 *>(y + col) = make_uint4(out[0], out[1], out[2], out[3]);
-    if (col + 8 < p.N) *reinterpret_cast<uint4 *>(y + col + 8) = make_uint4(out[4], out[5], out[6], out[7]);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(t[j].x, t[j].y);
+    out[j] = *reinterpret_cast<const uint32_t *>(&h);
   }
+}
+
+// Whether the phase of `bar` with parity `parity` has completed, without waiting.
+__device__ __forceinline__ uint32_t mbar_test(uint64_t *bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(dev::smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done;
 }
 
 template <int EPI>
@@ -129,13 +151,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     fp8_gemm_pair_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem + BAR_OFF);   // even CTA: both CTAs' bytes
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + BAR_OFF);  // even CTA: both CTAs' bytes
   uint64_t *empty = full + STAGES;                                  // both CTAs: stage free again
   uint64_t *sf_full = empty + STAGES;                               // even CTA: both CTAs' scale words
   uint64_t *sf_empty = sf_full + SF_BUFS;                           // both CTAs: their copy into TMEM is done
   uint64_t *sft_full = sf_empty + SF_BUFS;                          // even CTA: scale words in both TMEMs
   uint64_t *sft_empty = sft_full + SF_TMEM;                         // even CTA: their MMAs are done
-  uint64_t *tmem_full = sft_empty + SF_TMEM;                       // both CTAs: accumulator ready
+  uint64_t *tmem_full = sft_empty + SF_TMEM;                        // both CTAs: accumulator ready
   uint64_t *tmem_empty = tmem_full + 2;                             // even CTA: both CTAs drained it
   uint64_t *drain = tmem_empty + 2;
   uint64_t *drain_cp = drain + 1;
@@ -176,6 +198,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     dev::tmem_alloc_pair(tmem_slot, TMEM_COLS);
     dev::tmem_relinquish_pair();
   }
+  // The kernel in front is the quantizer, which lets this one start only after its own wait: everything older
+  // (offsets and weights among it) has completed by now, and only X's codes and scales have to be waited for,
+  // where they are first read.
   if (warp == 2) fill_expert_table(p, TOK, 8, tab);
   dev::tc_fence_before();
   __syncwarp();
@@ -190,15 +215,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     if (elect_one()) {
       dev::prefetch_tmap(&maps.x);
       dev::prefetch_tmap(&maps.w);
-      // the weights of the first unit's first stages, before the activations are there to wait for
-      int ahead = 0;
+      // rows past the end of a stage's rows hold the next stage's, past the buffer zeros: neither reaches an output
+      const auto load_weights = [&](const Item &u, int ks, int s) {
+        if (h == 0) dev::mbar_arrive_expect_tx(&full[s], 2u * STAGE);
+        dev::tma_load_2d_pair(smem + s * STAGE + X_BYTES, &maps.w, dev::mapa(dev::smem_u32(&full[s]), 0), 0,
+                              weight_row(p, u, ks, h));
+      };
+      int ahead = 0;                                 // stages whose weights are under way before X is there
       if (pair < items) {
         const Item u = find_item(p, tab, TOK, 8, ntn, pair);
-        for (; ahead < min(STAGES, p.KS); ++ahead) {
-          if (h == 0) dev::mbar_arrive_expect_tx(&full[ahead], 2u * STAGE);
-          dev::tma_load_2d_pair(smem + ahead * STAGE + X_BYTES, &maps.w, dev::mapa(dev::smem_u32(&full[ahead]), 0), 0,
-                                weight_row(p, u, ahead, h));
-        }
+        for (; ahead < min(STAGES, p.KS); ++ahead) load_weights(u, ahead, ahead);
       }
       dev::grid_dependency_wait();
       int it = 0;
@@ -208,69 +234,76 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const int xrow = u.row0 / 8 + 16 * static_cast<int>(h);
         for (int ks = 0; ks < p.KS; ++ks, ++it) {
           const int s = it % STAGES;
-          const uint32_t bar = dev::mapa(dev::smem_u32(&full[s]), 0);
-          uint8_t *dst = smem + s * STAGE;
-          // rows past the end of a stage's rows hold the next stage's, past the buffer zeros: neither reaches
-          // an output
           if (it >= ahead) {
-            if (!dev::mbar_wait_cluster(&empty[s], ((it / STAGES) & 1) ^ 1, p.limit_ns, abort_flag)) {
+            if (!dev::mbar_wait(&empty[s], ((it / STAGES) & 1) ^ 1, p.limit_ns, abort_flag)) {
               ok = false;
               break;
             }
-            if (h == 0) dev::mbar_arrive_expect_tx(&full[s], 2u * STAGE);
-            dev::tma_load_2d_pair(dst + X_BYTES, &maps.w, bar, 0, weight_row(p, u, ks, h));
+            load_weights(u, ks, s);
           }
-          dev::tma_load_2d_pair(dst, &maps.x, bar, 0, xrow + ks * (p.Mp / 8));
+          dev::tma_load_2d_pair(smem + s * STAGE, &maps.x, dev::mapa(dev::smem_u32(&full[s]), 0), 0,
+                                xrow + ks * (p.Mp / 8));
         }
       }
       if (!ok) abort_pair(abort_flag, peer_abort, p.status);
       // before the pair may leave, every stage the even CTA armed completes (the odd CTA's copies with it)
       if (h == 0)
         for (int j = max(0, it - STAGES); j < it; ++j)
-          dev::mbar_wait_cluster(&full[j % STAGES], (j / STAGES) & 1, p.limit_ns, nullptr);
+          dev::mbar_wait(&full[j % STAGES], (j / STAGES) & 1, p.limit_ns, nullptr);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ scales into TMEM, MMAs (even CTA)
     if (h == 0 && elect_one()) {
       constexpr uint32_t idesc = idesc_mxf8(TOK, TILE_N);
-      int it = 0, quad = 0, n = 0;
+      const uint64_t desc0 = dev::desc_sw128(dev::smem_u32(smem));
+      uint64_t dx = desc0;                           // the ring place's operands, its number and its phase
+      int s = 0;
+      uint32_t phase = 0, ready = 0;
+      int b = 0, n = 0;
+      uint32_t b_phase = 0;
       bool ok = true, issued = false;
       for (int item = pair; item < items && ok; item += pairs, ++n) {
         const int a = n & 1;
-        if (!dev::mbar_wait_cluster(&tmem_empty[a], ((n >> 1) & 1) ^ 1, p.limit_ns, abort_flag)) {
+        if (!dev::mbar_wait(&tmem_empty[a], ((n >> 1) & 1) ^ 1, p.limit_ns, abort_flag)) {
           ok = false;
           break;
         }
         dev::tc_fence_after();
         const uint32_t acc = tmem + a * TILE_N;
-        uint32_t sfx = 0, sfw = 0;
-        for (int ks = 0; ks < p.KS; ++ks, ++it) {
-          const int s = it % STAGES, b = quad % SF_TMEM;
-          if ((ks & 3) == 0) {
-            if (!dev::mbar_wait(&sft_full[b], (quad / SF_TMEM) & 1, p.limit_ns, abort_flag)) {
-              ok = false;
-              break;
-            }
-            sfx = tmem + SF_COL + 12 * b;
-            sfw = sfx + 4;
-          }
-          if (!dev::mbar_wait_cluster(&full[s], (it / STAGES) & 1, p.limit_ns, abort_flag)) {
+        uint32_t accumulate = 0;
+        for (int ks0 = 0; ks0 < p.KS && ok; ks0 += 4) {    // four stages under one set of scale words
+          if (!dev::mbar_wait(&sft_full[b], b_phase, p.limit_ns, abort_flag)) {
             ok = false;
             break;
           }
-          dev::tc_fence_after();
-          const uint32_t sx = dev::smem_u32(smem + s * STAGE), sw = sx + X_BYTES;
-          const uint32_t id = with_scale_bytes(idesc, ks & 3, ks & 3);
+          const uint32_t sf = tmem + SF_COL + SF_COLS * b;
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            umma_mxf8_pair(acc, dev::desc_sw128(sx + 32 * j), dev::desc_sw128(sw + 32 * j), id, sfx, sfw,
-                           ks > 0 || j > 0 ? 1u : 0u);
-          issued = true;
-          dev::tc_commit_pair_mc(&empty[s], 0x3);
-          if ((ks & 3) == 3 || ks == p.KS - 1) {
-            dev::tc_commit_pair(&sft_empty[b]);
-            ++quad;
+          for (int i = 0; i < 4; ++i) {
+            if (ks0 + i >= p.KS) break;
+            if (!ready && !dev::mbar_wait(&full[s], phase, p.limit_ns, abort_flag)) {
+              ok = false;
+              break;
+            }
+            dev::tc_fence_after();
+            const bool wrap = s == STAGES - 1;
+            const int next = wrap ? 0 : s + 1;
+            phase ^= wrap ? 1u : 0u;
+            ready = mbar_test(&full[next], phase);
+            const uint32_t id = with_scale_bytes(idesc, i, i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              umma_mxf8_pair(acc, dx + desc_step(32 * j), dx + desc_step(X_BYTES + 32 * j), id, sf, sf + 4, accumulate);
+              accumulate = 1;
+            }
+            issued = true;
+            dev::tc_commit_pair_mc(&empty[s], 0x3);
+            dx = wrap ? desc0 : dx + desc_step(STAGE);
+            s = next;
           }
+          if (!ok) break;
+          dev::tc_commit_pair(&sft_empty[b]);
+          b_phase ^= b == SF_TMEM - 1 ? 1u : 0u;
+          b = b == SF_TMEM - 1 ? 0 : b + 1;
         }
         if (!ok) break;
         dev::tc_commit_pair_mc(&tmem_full[a], 0x3);
@@ -284,41 +317,64 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   } else if (warp == 2) {
     // ------------------------------------------------------------ scale words (both CTAs)
     dev::grid_dependency_wait();
-    int quad = 0;
-    bool ok = true;
-    for (int item = pair; item < items && ok; item += pairs) {
-      const Item u = find_item(p, tab, TOK, 8, ntn, item);
-      for (int kw = 0; kw < p.KW; ++kw, ++quad) {
-        const int b = quad % SF_BUFS;
-        const uint32_t *xs = p.sx + static_cast<size_t>(kw) * p.Mp;
-        uint32_t xw[4], ww[8];
+    uint32_t xw[SF_BUFS][4], ww[SF_BUFS][8];
+    int item[SF_BUFS], kw[SF_BUFS];
+    Item u[SF_BUFS];
+    // `sets` sets on in the CTA's sequence, and the words of the set there
+    const auto advance = [&](int d, int sets) {
+      const int was = item[d];
+      for (kw[d] += sets; kw[d] >= p.KW; kw[d] -= p.KW) item[d] += pairs;
+      if (item[d] != was && item[d] < items) u[d] = find_item(p, tab, TOK, 8, ntn, item[d]);
+    };
+    const auto load = [&](int d) {
+      if (item[d] >= items) return;
+      const uint32_t *xs = p.sx + static_cast<size_t>(kw[d]) * p.Mp;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = u.row0 + 128 * static_cast<int>(h) + 32 * i + lane;
-          xw[i] = row < p.Mp ? xs[row] : 0u;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = 32 * i + lane, col = u.nt * TILE_N + r;
-          ww[i] = r < TILE_N && col < p.N
-                      ? __ldg(weight_atom(p, u.expert, col >> 7, kw) + (col & 31) * 4 + ((col >> 5) & 3))
-                      : 0u;
-        }
-        const bool got = dev::mbar_wait_cluster(&sf_empty[b], ((quad / SF_BUFS) & 1) ^ 1, p.limit_ns, abort_flag);
-        if (!__all_sync(0xFFFFFFFFu, got)) {
-          ok = false;
-          break;
-        }
-        uint4 *dst = reinterpret_cast<uint4 *>(smem + SF_OFF + b * SF_BYTES);
-        dst[lane] = make_uint4(xw[0], xw[1], xw[2], xw[3]);
-        dst[32 + lane] = make_uint4(ww[0], ww[1], ww[2], ww[3]);
-        dst[64 + lane] = make_uint4(ww[4], ww[5], ww[6], ww[7]);
-        dev::fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) dev::mbar_arrive_cluster(dev::mapa(dev::smem_u32(&sf_full[b]), 0));
+      for (int i = 0; i < 4; ++i) {
+        const int row = u[d].row0 + 128 * static_cast<int>(h) + 32 * i + lane;
+        xw[d][i] = row < p.Mp ? xs[row] : 0u;
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int col = u[d].nt * TILE_N + 32 * i + lane;
+        ww[d][i] = 32 * i + lane < TILE_N && col < p.N ? __ldg(weight_atom(p, u[d].expert, col >> 7, kw[d]) + (col & 31) * 4 + ((col >> 5) & 3)) : 0u;
+      }
+    };
+    if (pair < items) {
+      const Item first = find_item(p, tab, TOK, 8, ntn, pair);
+#pragma unroll
+      for (int d = 0; d < SF_BUFS; ++d) {
+        item[d] = pair;
+        kw[d] = 0;
+        u[d] = first;
+        advance(d, d);
+        load(d);
+      }
+      bool ok = true;
+      uint32_t phase = 1;
+      while (ok && item[0] < items) {
+#pragma unroll
+        for (int d = 0; d < SF_BUFS; ++d) {
+          if (!ok || item[d] >= items) break;
+          const bool got = dev::mbar_wait(&sf_empty[d], phase, p.limit_ns, abort_flag);
+          if (!__all_sync(0xFFFFFFFFu, got)) {
+            ok = false;
+            break;
+          }
+          uint4 *dst = reinterpret_cast<uint4 *>(smem + SF_OFF + d * SF_BYTES);
+          dst[lane] = make_uint4(xw[d][0], xw[d][1], xw[d][2], xw[d][3]);
+          dst[32 + lane] = make_uint4(ww[d][0], ww[d][1], ww[d][2], ww[d][3]);
+          dst[64 + lane] = make_uint4(ww[d][4], ww[d][5], ww[d][6], ww[d][7]);
+          dev::fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) dev::mbar_arrive_remote(dev::mapa(dev::smem_u32(&sf_full[d]), 0));
+          advance(d, SF_BUFS);
+          load(d);
+        }
+        phase ^= 1;
+      }
+      if (!ok && lane == 0) abort_pair(abort_flag, peer_abort, p.status);
     }
-    if (!ok && lane == 0) abort_pair(abort_flag, peer_abort, p.status);
   } else if (warp == 3) {
     // ------------------------------------------------------------ scale words into TMEM (even CTA)
     // from a warp of its own: in the MMA thread's order the copies would stand between the MMAs
@@ -328,17 +384,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       for (int item = pair; item < items && ok; item += pairs) {
         for (int kw = 0; kw < p.KW; ++kw, ++quad) {
           const int b = quad % SF_BUFS, t = quad % SF_TMEM;
-          if (!dev::mbar_wait_cluster(&sf_full[b], (quad / SF_BUFS) & 1, p.limit_ns, abort_flag) ||
+          if (!dev::mbar_wait(&sf_full[b], (quad / SF_BUFS) & 1, p.limit_ns, abort_flag) ||
               !dev::mbar_wait(&sft_empty[t], ((quad / SF_TMEM) & 1) ^ 1, p.limit_ns, abort_flag)) {
             ok = false;
             break;
           }
           dev::tc_fence_after();
           const uint32_t src = dev::smem_u32(smem + SF_OFF + b * SF_BYTES);
-          const uint32_t dst = tmem + SF_COL + 12 * t;
-          dev::tmem_cp_32x128b_x4_pair(dst, dev::desc_sf(src));
-          dev::tmem_cp_32x128b_x4_pair(dst + 4, dev::desc_sf(src + kScaleAtom));
-          dev::tmem_cp_32x128b_x4_pair(dst + 8, dev::desc_sf(src + 2 * kScaleAtom));
+          const uint32_t dst = tmem + SF_COL + SF_COLS * t;
+#pragma unroll
+          for (int i = 0; i < 3; ++i) dev::tmem_cp_32x128b_x4_pair(dst + 4 * i, dev::desc_sf(src + i * kScaleAtom));
           dev::tc_commit_pair(&sft_full[t]);
           dev::tc_commit_pair_mc(&sf_empty[b], 0x3);
         }
@@ -351,42 +406,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue (both CTAs)
-    const int e = warp - 4, q = warp & 3, half = e >> 2;   // TMEM lane quarter; columns 0..127 or 128..239
+    const int e = warp - 4, q = warp & 3, part = e >> 2;   // TMEM lane quarter; 64 columns, or the last 48
+    const int begin = 64 * part, cols = min(64, TILE_N - begin);
+    uint8_t *stage = smem + EPI_OFF + e * EPI_TILE;
     const uint32_t tmem_empty_even = dev::mapa(dev::smem_u32(tmem_empty), 0);
-    const bool wide = ((reinterpret_cast<uintptr_t>(p.Y) | (p.ldy * 2)) & 31) == 0;
     dev::grid_dependency_wait();
     int n = 0;
     for (int item = pair; item < items; item += pairs, ++n) {
       const Item u = find_item(p, tab, TOK, 8, ntn, item);
-      const int a = n & 1;
-      const bool got = dev::mbar_wait_cluster(&tmem_full[a], (n >> 1) & 1, p.limit_ns, abort_flag);
+      const int row0 = u.row0 + 128 * static_cast<int>(h) + 32 * q, a = n & 1;
+      const int col0 = u.nt * TILE_N + begin;
+      const uint16_t *bias = p.bias ? p.bias + static_cast<size_t>(u.expert) * p.N + col0 : nullptr;
+      // the warp's columns that exist, none if none of its 32 rows is the expert's
+      const int live = row0 >= u.end ? 0 : min(cols, p.N - col0);
+      const int t0 = lane >> 2, seg = lane & 3;
+      uint16_t *yrow = p.Y + static_cast<size_t>(row0 + t0) * p.ldy + col0 + 8 * seg;
+      const bool got = dev::mbar_wait(&tmem_full[a], (n >> 1) & 1, p.limit_ns, abort_flag);
       if (!__all_sync(0xFFFFFFFFu, got)) {
         if (lane == 0) abort_pair(abort_flag, peer_abort, p.status);
         break;
       }
       dev::tc_fence_after();
-      const int row = u.row0 + 128 * static_cast<int>(h) + 32 * q + lane;
-      const bool row_ok = row >= u.begin && row < u.end;
-      uint16_t *y = p.Y + static_cast<size_t>(row) * p.ldy;
-      const uint16_t *bias = p.bias ? p.bias + static_cast<size_t>(u.expert) * p.N : nullptr;
-      const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(a * TILE_N);
-      if (row - lane < u.end) {                            // some row of this warp's 32 is the expert's
+      const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(a * TILE_N + begin);
 #pragma unroll 1
-        for (int c = 128 * half; c < (half ? TILE_N : 128); c += 32) {
-          const int col = u.nt * TILE_N + c;
-          if (col >= p.N) break;                           // the whole warp
-          const bool two = c + 16 < TILE_N;
-          uint32_t v0[16], v1[16];
-          tmem_ld_32x32b_x16(taddr + c, v0);
-          if (two) tmem_ld_32x32b_x16(taddr + c + 16, v1);
-          dev::tmem_wait_ld();
-          finish16<EPI>(p, bias, v0, col, y, row_ok, wide);
-          if (two && col + 16 < p.N) finish16<EPI>(p, bias, v1, col + 16, y, row_ok, wide);
+      for (int c = 0; c < live; c += 16) {
+        uint32_t v[16], out[8];
+        tmem_ld_32x32b_x16(taddr + c, v);
+        uint4 bb[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+        if (bias) {
+          bb[0] = __ldg(reinterpret_cast<const uint4 *>(bias + c));
+          if (c + 8 < live) bb[1] = __ldg(reinterpret_cast<const uint4 *>(bias + c + 8));   // N % 8 == 0
+        }
+        dev::tmem_wait_ld();
+        finish16<EPI>(v, bb, p.gelu_col_begin - col0 - c, out);
+        // row `lane`, 16-byte chunk k of the 32 columns at chunk k ^ (row / 2 % 4): few bank conflicts either way
+        const int k = (c & 16) >> 3, x = (lane >> 1) & 3;
+        *reinterpret_cast<uint4 *>(stage + lane * 64 + ((k ^ x) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
+        *reinterpret_cast<uint4 *>(stage + lane * 64 + (((k + 1) ^ x) << 4)) = make_uint4(out[4], out[5], out[6], out[7]);
+        if ((c & 16) != 0 || c + 16 >= live) {             // 32 columns, or the last: 8 rows at a time
+          const int c32 = c & ~31;
+          const bool there = c32 + 8 * seg < live;
+          __syncwarp();
+          uint16_t *y = yrow + c32;
+#pragma unroll
+          for (int i = 0; i < 4; ++i, y += 8 * p.ldy) {
+            const int t = 8 * i + t0, row = row0 + t;
+            if (there && row >= u.begin && row < u.end)
+              *reinterpret_cast<uint4 *>(y) = *reinterpret_cast<const uint4 *>(stage + t * 64 + ((seg ^ ((t >> 1) & 3)) << 4));
+          }
+          __syncwarp();
         }
       }
       dev::tc_fence_before();
       __syncwarp();
-      if (lane == 0) dev::mbar_arrive_cluster(tmem_empty_even + 8 * a);
+      if (lane == 0) dev::mbar_arrive_remote(tmem_empty_even + 8 * a);
     }
   }
 
@@ -422,7 +495,9 @@ int launch_gemm_pair(const char *fn, const Params &p, int epilogue, int sm_count
     rc = encode_tmap_2d(&maps.w, u64, p.w, MAP_ROW / 8, static_cast<uint64_t>(p.experts) * p.KS * (p.N / 8), MAP_ROW,
                         MAP_ROW / 8, W_BYTES / MAP_ROW, none);
   if (rc != SVDQ_OK) return rc;
-  const long long units = (p.M / TOK + (p.offsets ? 2ll * p.experts : 1ll)) * ((p.N + TILE_N - 1) / TILE_N);
+  // token tiles: one per 256 rows, and two that each expert may leave unfilled
+  const long long tiles = p.offsets ? p.M / TOK + 2ll * p.experts : (p.M + TOK - 1) / TOK;
+  const long long units = tiles * ((p.N + TILE_N - 1) / TILE_N);
   const int pairs = static_cast<int>(units < sm_count / 2 ? units : sm_count / 2);
   return epilogue == SVDQ_EPILOGUE_GELU_ERF    ? launch<SVDQ_EPILOGUE_GELU_ERF>(fn, p, maps, pairs, stream)
          : epilogue == SVDQ_EPILOGUE_GELU_TANH ? launch<SVDQ_EPILOGUE_GELU_TANH>(fn, p, maps, pairs, stream)
