@@ -1,7 +1,8 @@
 // Block-scaled FP8 linear layer: the entry points.  Few rows (an average share
-// of at most 128 an expert) run in the kernel of weight-bound calls, which
-// quantizes X itself if they are very few; otherwise a quantizer runs in front,
-// and many rows go through 256-row tiles on SM pairs.
+// of at most 128 an expert, more where its tiles fill the SMs better) run in the
+// kernel of weight-bound calls, which quantizes X itself if they are very few;
+// otherwise a quantizer runs in front, and many rows go through 256-row tiles
+// on SM pairs.
 #include <cuda_runtime.h>
 
 #include <string>
@@ -13,10 +14,23 @@ namespace fp8 {
 
 int launch_quantize_act(const char *fn, const void *X, int M, int K, int ldx, void *workspace, int sm_count,
                         cudaStream_t stream);
-int launch_gemm_few(const char *fn, const Params &p, int epilogue, int sm_count, cudaStream_t stream);
+int launch_gemm_few(const char *fn, const Params &p, int tile, int epilogue, int sm_count, cudaStream_t stream);
 int launch_gemm_pair(const char *fn, const Params &p, int epilogue, int sm_count, cudaStream_t stream);
 
 namespace {
+
+// Whether 128-row tiles of the few-row kernel beat 256-row tiles on SM pairs for more rows than 128.  Per stage of
+// 128 along K a round of theirs takes about 0.285 us (a unit an SM) against 0.365 us (a unit a pair), and the pairs'
+// start and end take 4 us more.  Measured, K = 2560, few rows / pairs: 256 rows -> 7680 11.7 / 15.5 us, 768 rows ->
+// 7680 22.6 / 22.9 us, 512 rows -> 15360 28.2 / 24.1 us; 4096 -> 2560: 512 rows 14.5 / 18.5 us.
+bool few_is_faster(const Params &p, int sm_count) {
+  const long long half = p.offsets ? p.experts / 2 : 0;      // what ragged experts leave unfilled on average
+  const long long few_tiles = p.offsets ? p.M / 128 + half + 1 : (p.M + 127) / 128;
+  const long long pair_tiles = p.offsets ? p.M / 256 + half + 1 : (p.M + 255) / 256;
+  const long long few_rounds = (few_tiles * ((p.N + 127) / 128) + sm_count - 1) / sm_count;
+  const long long pairs = sm_count / 2, pair_rounds = (pair_tiles * ((p.N + 239) / 240) + pairs - 1) / pairs;
+  return 57 * p.KS * few_rounds < 73 * p.KS * pair_rounds + 800;
+}
 
 int run(const char *fn, const void *X, int M, int K, int ldx, const int *offsets, int experts, const void *packed,
         const void *bias, int N, int epilogue, int gelu_col_begin, void *Y, int ldy, void *workspace,
@@ -68,9 +82,11 @@ int run(const char *fn, const void *X, int M, int K, int ldx, const int *offsets
     p.sx = reinterpret_cast<const uint32_t *>(p.x + act_code_bytes(M, K));
     rc = launch_quantize_act(fn, X, M, K, ldx, workspace, st->sm_count, stream);
   }
+  int tile = few_tile(M, experts);
+  if (tile == 0 && few_is_faster(p, st->sm_count)) tile = 128;
   if (rc == SVDQ_OK)
-    rc = few_tile(row_share(M, experts)) ? launch_gemm_few(fn, p, epilogue, st->sm_count, stream)
-                                         : launch_gemm_pair(fn, p, epilogue, st->sm_count, stream);
+    rc = tile ? launch_gemm_few(fn, p, tile, epilogue, st->sm_count, stream)
+              : launch_gemm_pair(fn, p, epilogue, st->sm_count, stream);
   return rc == SVDQ_OK ? ok() : rc;
 }
 

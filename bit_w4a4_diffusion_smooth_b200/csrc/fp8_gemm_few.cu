@@ -577,8 +577,7 @@ int launch(const char *fn, const Params &p, int epilogue, int sm_count, cudaStre
 
 }  // namespace
 
-int launch_gemm_few(const char *fn, const Params &p, int epilogue, int sm_count, cudaStream_t stream) {
-  const int tile = few_tile(row_share(p.M, p.experts));
+int launch_gemm_few(const char *fn, const Params &p, int tile, int epilogue, int sm_count, cudaStream_t stream) {
   return tile == 16   ? launch<16>(fn, p, epilogue, sm_count, stream)
          : tile == 32 ? launch<32>(fn, p, epilogue, sm_count, stream)
          : tile == 64 ? launch<64>(fn, p, epilogue, sm_count, stream)

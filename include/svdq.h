@@ -556,8 +556,7 @@ int svdq_linear_int4(const uint8_t *a_codes, const void *a_scales, const void *U
 int fp8_weight_size(int K, int N, int experts, size_t *bytes);
 
 /* Bytes of the workspace of a call: the quantized activations, or 0 where the
- * call quantizes them on the way in (an average share of at most 16 rows an
- * expert).  Rules: M >= 1, K >= 8, K % 8 == 0, 1 <= experts <= FP8_MAX_EXPERTS. */
+ * call quantizes them on the way in (16 rows, or 8 an expert on average).  Rules: M >= 1, K >= 8, K % 8 == 0, 1 <= experts <= FP8_MAX_EXPERTS. */
 int fp8_workspace_size(int M, int K, int experts, size_t *bytes);
 
 /*

@@ -16,8 +16,8 @@ def test_sizes():
     assert lib.fp8_weight_size(136, 136, 3) == 3 * (136 * 2 * 128 + 2 * 512)
     assert lib.fp8_workspace_size(1001, 136) == 2 * 1008 * 128 + 1008 * 4
     assert lib.fp8_workspace_size(129, 8) == 136 * 128 + 136 * 4
-    assert lib.fp8_workspace_size(16, 136) == lib.fp8_workspace_size(128, 136, 8) == 0
-    assert lib.fp8_workspace_size(17, 136) > 0 and lib.fp8_workspace_size(129, 136, 8) > 0
+    assert lib.fp8_workspace_size(16, 136) == lib.fp8_workspace_size(64, 136, 8) == 0
+    assert lib.fp8_workspace_size(17, 136) > 0 and lib.fp8_workspace_size(65, 136, 8) > 0
     for bad in ((0, 8), (12, 8), (8, 0), (8, 12), (8, 8, 0), (8, 8, 513)):
         with pytest.raises(lib.SvdqError) as e:
             lib.fp8_weight_size(*bad)

@@ -97,16 +97,19 @@ def test_linear(M, K, N, epilogue):
 
 
 @pytest.mark.parametrize("M,K,N", [(1, 8, 8), (5, 128, 128), (20, 8, 4104), (100, 2560, 512), (700, 4096, 264),
-                                   (1000, 72, 1032), (257, 1024, 512), (513, 640, 768)])
+                                   (1000, 72, 1032), (257, 1024, 512), (513, 640, 768),
+                                   # wide enough for the SM pairs' 256 x 240 tiles: one stage, a short last set of
+                                   # scale words, several tiles a pair, ragged rows and columns
+                                   (4000, 128, 9608), (2600, 1416, 5640), (5001, 640, 7688), (9000, 264, 3608)])
 def test_linear_shapes(M, K, N):
     x, w = rand(M + 1, M, K), rand(K + 1, K, N, scale=0.05, loud=False)
     Y, _ = run_linear(x, w, None)
     close(Y, *fp8.linear(x, w), K, 0)
 
 
-@pytest.mark.parametrize("M", [3, 40, 200, 600])
-def test_linear_strides_gelu_begin_and_untouched_bytes(M):
-    K, N = 264, 392
+@pytest.mark.parametrize("M,N", [(3, 392), (40, 392), (200, 392), (600, 392), (3001, 7688)])
+def test_linear_strides_gelu_begin_and_untouched_bytes(M, N):
+    K = 264
     x, w, b = rand(5, M, K), rand(6, K, N, scale=0.05, loud=False), rand(7, N, loud=False)
     Y, Yf = run_linear(x, w, b, 1, 130, ldx=K + 24, ldy=N + 40)
     want, mag = fp8.linear(x, w, b, 1, 130)
@@ -114,22 +117,22 @@ def test_linear_strides_gelu_begin_and_untouched_bytes(M):
     assert torch.isnan(Yf[:, N:]).all()
 
 
-@pytest.mark.parametrize("M", [1, 24, 130, 1030])
-def test_linear_exact_on_small_integers(M):
+@pytest.mark.parametrize("M,N", [(1, 400), (24, 400), (130, 400), (1030, 400), (2500, 8000)])
+def test_linear_exact_on_small_integers(M, N):
     """Integers up to 8 are e4m3 values under any scale that keeps them normal; their sums fit 24 bits, so the
     result is the exact sum's bf16."""
     r = np.random.default_rng(M)
-    K, N = 1304, 400
+    K = 1304
     x, w = r.integers(-8, 9, size=(M, K)).astype(float), r.integers(-8, 9, size=(K, N)).astype(float)
     Y, _ = run_linear(x, w, None)
     assert torch.equal(Y.cpu(), bf16(x @ w))
 
 
-@pytest.mark.parametrize("M", [4, 150])
-def test_scales_of_every_block_and_row(M):
+@pytest.mark.parametrize("M,N", [(4, 264), (150, 264), (1100, 264), (4000, 6008)])
+def test_scales_of_every_block_and_row(M, N):
     """Each row and each block of 128 at a magnitude of its own: a scale taken for another row or block shows."""
     r = np.random.default_rng(3)
-    K, N = 1160, 264
+    K = 1160
     KS = -(-K // 128)
     x = r.integers(1, 3, size=(M, K)) * np.exp2(r.integers(-3, 4, size=(M, KS)).astype(float)).repeat(128, 1)[:, :K]
     w = r.integers(1, 3, size=(K, N)) * np.exp2(r.integers(-3, 4, size=(KS, N)).astype(float)).repeat(128, 0)[:K]
@@ -173,10 +176,10 @@ def run_experts(x, w, offsets, b=None, epilogue=0, begin=0):
 
 @pytest.mark.parametrize("counts,tail", [
     ([1], 0), ([0, 3, 0, 0, 9, 1, 0], 0), ([0, 0, 0], 5), ([17, 0, 130, 1, 31, 8], 3), ([300, 5, 0, 77], 0),
-    ([0] * 40 + [2] + [0] * 30 + [3], 1), ([7] * 33, 2), ([513, 1, 255, 0, 256], 11), ([1] * 100, 0)])
+    ([0] * 40 + [2] + [0] * 30 + [3], 1), ([7] * 33, 2), ([513, 1, 255, 0, 256], 11), ([1] * 100, 0), ([1500, 0, 257, 1, 2000, 903], 5)])
 @pytest.mark.parametrize("epilogue", EPI)
 def test_experts(counts, tail, epilogue):
-    E, K, N = len(counts), 264, 136
+    E, K, N = len(counts), 264, 136 if sum(counts) < 4000 else 5000     # the last: 256-row tiles on SM pairs
     T = sum(counts) + tail
     off = np.concatenate([[0], np.cumsum(counts)])
     x, w, b = rand(T, T, K), rand(E, E, K, N, scale=0.05, loud=False), rand(E + 1, E, N, loud=False)
@@ -336,8 +339,8 @@ def test_offsets_from_the_kernel_before():
 
 def test_repeats_are_bit_identical():
     x = bf16(rand(1, 333, 1000)).to(G.DEV)
-    for m in (1, 20, 333):
-        lin = layer.FP8Linear(bf16(rand(2, 1000, 520, scale=0.05, loud=False)).to(G.DEV))
+    for m, n in ((1, 520), (20, 520), (333, 520), (333, 33000)):
+        lin = layer.FP8Linear(bf16(rand(2, 1000, n, scale=0.05, loud=False)).to(G.DEV))
         first = lin(x[:m])
         for _ in range(10):
             assert torch.equal(lin(x[:m]), first)
