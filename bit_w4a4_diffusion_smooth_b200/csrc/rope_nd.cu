@@ -17,6 +17,12 @@
 // Bound by memory: each element is read and written once (4 bytes).  A lane
 // holds 4 pairs of a head (8 elements): 16 contiguous bytes in the interleaved
 // pairing (2i, 2i + 1), two runs of 8 bytes in the half-split one (i, i + D/2).
+// A group of lanes keeps one token's cos and sin, times the norm weights of one
+// tensor, in registers and walks over that tensor's heads, four heads' loads in
+// flight at a time; the first four are under way while the block computes its
+// angles.  The arithmetic runs on f32x2 instructions, two pairs at once: with
+// scalar ones, and the tensor chosen head by head, the normed call was bound by
+// issue (4608 rows x 40 heads x 128: 30 us).
 #include <cuda_runtime.h>
 
 #include <string>
@@ -28,7 +34,7 @@ namespace svdq {
 namespace rope {
 namespace {
 
-constexpr int THREADS = 256;
+constexpr int THREADS = 128;      // (256: 22.2 us where 128 take 20.5, 4608 normed rows x 40 heads x 128)
 constexpr int MAX_D = 256;
 
 struct Tensor {
@@ -42,9 +48,11 @@ struct Params {
   Tensor t[2];                  // query, key (heads 0 when absent)
   const void *pos;              // [M][pos_row]: int32 or float32
   long long pos_row;
-  int M, D, tokens, group_log2; // tokens per block; log2 of the lanes per head
+  int M, D;
+  int lanes_log2, groups_log2;  // log2 of the lanes per head and of the groups per token
+  int q_groups;                 // of which the first so many take the query's heads
   int pos_float, inverse;
-  float eps;
+  float eps, inv_d;
   double freq[MAX_D / 2];
   unsigned char axis[MAX_D / 2];
 };
@@ -74,90 +82,158 @@ __device__ __forceinline__ void store8(uint16_t *p, int c, int D, const uint32_t
     *reinterpret_cast<uint4 *>(p + 8 * c) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
-__device__ __forceinline__ void widen(const uint32_t (&w)[4], float (&f)[8]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-}
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+constexpr int UNROLL = 4;
+
+// The 4 pairs of a lane as two sets of two: first and second elements.
 template <bool HALF>
+__device__ __forceinline__ void split(const uint32_t (&w)[4], float2 (&x0)[2], float2 (&x1)[2]) {
+  const auto lo = [](uint32_t v) { return __uint_as_float(v << 16); };
+  const auto hi = [](uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); };
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if constexpr (HALF) {                     // words 0, 1: first elements; 2, 3: second elements
+      x0[i] = make_float2(lo(w[i]), hi(w[i]));
+      x1[i] = make_float2(lo(w[2 + i]), hi(w[2 + i]));
+    } else {                                  // a word is a pair
+      x0[i] = make_float2(lo(w[2 * i]), lo(w[2 * i + 1]));
+      x1[i] = make_float2(hi(w[2 * i]), hi(w[2 * i + 1]));
+    }
+  }
+}
+
+template <bool HALF, bool NORM>
 __global__ void __launch_bounds__(THREADS) rope_nd_kernel(const __grid_constant__ Params p) {
   extern __shared__ float2 turn[];            // [tokens][D/2] (cos, sin)
   dev::grid_dependency_wait();
   dev::grid_launch_dependents();
-  const int half_d = p.D / 2;
-  const int m0 = static_cast<int>(blockIdx.x) * p.tokens;
-  const int live = min(p.tokens, p.M - m0);
-  for (int i = threadIdx.x; i < live * half_d; i += THREADS) {
-    const int tok = i / half_d, pair = i % half_d;
-    const long long at = static_cast<long long>(m0 + tok) * p.pos_row + p.axis[pair];
+  const int half_d = p.D / 2, lanes = 1 << p.lanes_log2;
+  const int tokens = THREADS >> (p.lanes_log2 + p.groups_log2);
+  const int m0 = static_cast<int>(blockIdx.x) * tokens;
+  const int c = threadIdx.x & (lanes - 1);                              // 8 elements of a head; past D / 8 idle
+  const int group = (threadIdx.x >> p.lanes_log2) & ((1 << p.groups_log2) - 1);
+  const int tok = threadIdx.x >> (p.lanes_log2 + p.groups_log2);
+  const bool on = c < p.D / 8 && m0 + tok < p.M;
+  const long long m = m0 + tok;
+  // this group's tensor, its first head and the step to the next
+  const bool is_q = group < p.q_groups;
+  const Tensor &t = p.t[is_q ? 0 : 1];
+  const int first = is_q ? group : group - p.q_groups;
+  const int step = is_q ? p.q_groups : (1 << p.groups_log2) - p.q_groups, heads = on ? t.heads : 0;
+  // the same number of rounds for every lane: the norm's shuffles need full warps
+  const int k_groups = (1 << p.groups_log2) - p.q_groups;
+  const int rounds = max((p.t[0].heads + p.q_groups - 1) / p.q_groups, k_groups ? (p.t[1].heads + k_groups - 1) / k_groups : 0);
+  const uint16_t *x = t.x + m * t.x_row;
+  uint16_t *y = t.y + m * t.y_row;
+
+  uint32_t w[UNROLL][4];
+  const auto load = [&](int round) {
+#pragma unroll
+    for (int i = 0; i < UNROLL; ++i) {
+      const int h = first + (round + i) * step;
+      if (h < heads) {
+        load8<HALF>(x + h * t.x_head, c, p.D, w[i]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[i][k] = 0u;
+      }
+    }
+  };
+  load(0);
+
+  for (int i = threadIdx.x; i < min(tokens, p.M - m0) * half_d; i += THREADS) {
+    const int tk = i / half_d, pair = i % half_d;
+    const long long at = static_cast<long long>(m0 + tk) * p.pos_row + p.axis[pair];
     const double pos = p.pos_float ? static_cast<double>(__ldg(static_cast<const float *>(p.pos) + at))
                                    : static_cast<double>(__ldg(static_cast<const int *>(p.pos) + at));
-    double s, c;
-    sincos(pos * p.freq[pair], &s, &c);
-    turn[i] = make_float2(static_cast<float>(c), static_cast<float>(p.inverse ? -s : s));
+    double s, cs;
+    sincos(pos * p.freq[pair], &s, &cs);
+    turn[i] = make_float2(static_cast<float>(cs), static_cast<float>(p.inverse ? -s : s));
   }
   __syncthreads();
-
-  // a group of 2^group_log2 lanes per head vector, the lanes past D/8 idle
-  const int lanes = 1 << p.group_log2, c = threadIdx.x & (lanes - 1);
-  const int groups = THREADS >> p.group_log2;
-  const bool on = c < p.D / 8;
-  const int heads = p.t[0].heads + p.t[1].heads;
-  const int total = live * heads;
-  const int rounds = (total + groups - 1) / groups;   // the same for all lanes: the norm's shuffles need full warps
-  for (int r = 0; r < rounds; ++r) {
-    const int v = r * groups + static_cast<int>(threadIdx.x >> p.group_log2);
-    const bool act = on && v < total;
-    const int tok = act ? v / heads : 0, h = act ? v % heads : 0;
-    const Tensor &t = p.t[h < p.t[0].heads ? 0 : 1];
-    const int th = h < p.t[0].heads ? h : h - p.t[0].heads;
-    uint32_t w[4] = {0, 0, 0, 0};
-    if (act) load8<HALF>(t.x + (m0 + tok) * t.x_row + th * t.x_head, c, p.D, w);
-    float f[8];
-    widen(w, f);
-    float scale = 1.0f;
-    if (p.t[0].norm || p.t[1].norm) {
-      float sum = 0.0f;
+  // y0 = x0 c0 - x1 s1, y1 = x0 s0 + x1 c1: cos and sin, with the norm weight of the element they multiply
+  float2 c0[2], s0[2], c1[2], s1[2];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fmaf(f[i], f[i], sum);
-      for (int o = lanes >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-      scale = rsqrtf(sum / static_cast<float>(p.D) + p.eps);
-    }
-    if (!act) continue;
-    if (t.norm) {
+  for (int i = 0; i < 2; ++i) {
+    const float2 a = on ? turn[tok * half_d + 4 * c + 2 * i] : make_float2(0.0f, 0.0f);
+    const float2 b = on ? turn[tok * half_d + 4 * c + 2 * i + 1] : make_float2(0.0f, 0.0f);
+    c0[i] = c1[i] = make_float2(a.x, b.x);
+    s0[i] = s1[i] = make_float2(a.y, b.y);
+  }
+  const bool normed = NORM && t.norm != nullptr;
+  if constexpr (NORM) {
+    if (on && normed) {
       uint32_t nw[4];
       load8<HALF>(t.norm, c, p.D, nw);
-      float g[8];
-      widen(nw, g);
+      float2 g0[2], g1[2];
+      split<HALF>(nw, g0, g1);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = f[i] * scale * g[i];
-    }
-    const float2 *cs = turn + tok * half_d + 4 * c;
-    uint32_t out[4];
-    if constexpr (HALF) {
-      float a[4], b[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        a[i] = f[i] * cs[i].x - f[4 + i] * cs[i].y;
-        b[i] = f[i] * cs[i].y + f[4 + i] * cs[i].x;
+      for (int i = 0; i < 2; ++i) {
+        c0[i] = dev::mul2_rn(c0[i], g0[i]);
+        s0[i] = dev::mul2_rn(s0[i], g0[i]);
+        c1[i] = dev::mul2_rn(c1[i], g1[i]);
+        s1[i] = dev::mul2_rn(s1[i], g1[i]);
       }
-      out[0] = pack2(a[0], a[1]);
-      out[1] = pack2(a[2], a[3]);
-      out[2] = pack2(b[0], b[1]);
-      out[3] = pack2(b[2], b[3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        out[i] = pack2(f[2 * i] * cs[i].x - f[2 * i + 1] * cs[i].y, f[2 * i] * cs[i].y + f[2 * i + 1] * cs[i].x);
     }
-    store8<HALF>(t.y + (m0 + tok) * t.y_row + th * t.y_head, c, p.D, out);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) s1[i] = make_float2(-s1[i].x, -s1[i].y);
+
+  for (int round = 0; round < rounds; round += UNROLL) {
+    uint32_t out[UNROLL][4];
+    float scale[UNROLL];
+    if constexpr (NORM) {                     // four heads' sums side by side: their shuffles overlap
+#pragma unroll
+      for (int i = 0; i < UNROLL; ++i) {
+        float2 x0[2], x1[2];
+        split<HALF>(w[i], x0, x1);
+        float2 sum = dev::mul2_rn(x0[0], x0[0]);
+        sum = dev::fma2_rn(x1[0], x1[0], sum);
+        sum = dev::fma2_rn(x0[1], x0[1], sum);
+        sum = dev::fma2_rn(x1[1], x1[1], sum);
+        scale[i] = sum.x + sum.y;
+      }
+      for (int o = lanes >> 1; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < UNROLL; ++i) scale[i] += __shfl_xor_sync(0xFFFFFFFFu, scale[i], o);
+#pragma unroll
+      for (int i = 0; i < UNROLL; ++i) scale[i] = normed ? rsqrtf(fmaf(scale[i], p.inv_d, p.eps)) : 1.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < UNROLL; ++i) {
+      float2 x0[2], x1[2], y0[2], y1[2];
+      split<HALF>(w[i], x0, x1);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        y0[k] = dev::fma2_rn(x1[k], s1[k], dev::mul2_rn(x0[k], c0[k]));
+        y1[k] = dev::fma2_rn(x1[k], c1[k], dev::mul2_rn(x0[k], s0[k]));
+        if constexpr (NORM) {
+          y0[k] = dev::mul2_rn(y0[k], make_float2(scale[i], scale[i]));
+          y1[k] = dev::mul2_rn(y1[k], make_float2(scale[i], scale[i]));
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if constexpr (HALF) {
+          out[i][k] = pack2(y0[k].x, y0[k].y);
+          out[i][2 + k] = pack2(y1[k].x, y1[k].y);
+        } else {
+          out[i][2 * k] = pack2(y0[k].x, y1[k].x);
+          out[i][2 * k + 1] = pack2(y0[k].y, y1[k].y);
+        }
+      }
+    }
+    // the next heads' loads before these stores: no lane stores what another loads
+    if (round + UNROLL < rounds) load(round + UNROLL);
+#pragma unroll
+    for (int i = 0; i < UNROLL; ++i) {
+      const int h = first + (round + i) * step;
+      if (h < heads) store8<HALF>(y + h * t.y_head, c, p.D, out[i]);
+    }
   }
 }
 
@@ -227,14 +303,33 @@ extern "C" int rope_nd(const rope_nd_tensor_t *Q, const rope_nd_tensor_t *K, int
   p.pos_float = pos_is_float;
   p.inverse = inverse;
   p.eps = eps;
-  while ((1 << p.group_log2) < D / 8) ++p.group_log2;
-  // one angle per thread: as many tokens a block as have THREADS pairs together, unless that leaves SMs idle
-  p.tokens = M >= 4 * st->sm_count ? (2 * THREADS + D - 1) / D : 1;
-  const int blocks = (M + p.tokens - 1) / p.tokens;
-  const size_t smem = static_cast<size_t>(p.tokens) * (D / 2) * sizeof(float2);
-  DependentLaunch dl(dim3(blocks), dim3(THREADS), smem, stream);
-  cudaError_t e = plan->pairing == ROPE_ND_HALF ? cudaLaunchKernelEx(&dl.cfg, rope_nd_kernel<true>, p)
-                                                : cudaLaunchKernelEx(&dl.cfg, rope_nd_kernel<false>, p);
+  p.inv_d = 1.0f / static_cast<float>(D);
+  while ((1 << p.lanes_log2) < D / 8) ++p.lanes_log2;
+  // Groups per token: four, which with a block's tokens makes one angle a thread (more tokens a block would compute
+  // more); more while that leaves SMs without a block or two.  Each tensor's heads take a share of the groups by
+  // their number.
+  const int hq = Q->heads, hk = K ? K->heads : 0, most = 7 - p.lanes_log2;   // log2 of a block's groups
+  const auto blocks_at = [&](int g) {
+    const int tokens = 1 << (most - g);
+    return (M + tokens - 1) / tokens;
+  };
+  p.groups_log2 = most < 2 ? most : 2;
+  while (p.groups_log2 < most && (2 << p.groups_log2) <= hq + hk && blocks_at(p.groups_log2) < 2 * st->sm_count)
+    ++p.groups_log2;
+  const int groups = 1 << p.groups_log2;
+  p.q_groups = groups;
+  if (hk) {
+    p.q_groups = (groups * hq + (hq + hk) / 2) / (hq + hk);
+    p.q_groups = p.q_groups < 1 ? 1 : p.q_groups > groups - 1 ? groups - 1 : p.q_groups;
+  }
+  const size_t smem = (static_cast<size_t>(1) << (most - p.groups_log2)) * (D / 2) * sizeof(float2);
+  DependentLaunch dl(dim3(blocks_at(p.groups_log2)), dim3(THREADS), smem, stream);
+  const bool norm = Q->norm || (K && K->norm);
+  cudaError_t e = plan->pairing == ROPE_ND_HALF
+                      ? (norm ? cudaLaunchKernelEx(&dl.cfg, rope_nd_kernel<true, true>, p)
+                              : cudaLaunchKernelEx(&dl.cfg, rope_nd_kernel<true, false>, p))
+                      : (norm ? cudaLaunchKernelEx(&dl.cfg, rope_nd_kernel<false, true>, p)
+                              : cudaLaunchKernelEx(&dl.cfg, rope_nd_kernel<false, false>, p));
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return fail(SVDQ_ERR_CUDA, std::string("rope_nd launch: ") + cudaGetErrorString(e));
   return ok();

@@ -333,15 +333,15 @@ class AWQLinear:
 def _on(device, stream, call, *args):
     """call(*args, raw stream) with `device` current and torch allocating on the stream the work runs on: `stream`,
     else the caller's current stream of that device."""
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the layer on {device}")
-        with torch.cuda.stream(stream):       # makes the stream's device current as well
-            return call(*args, stream.cuda_stream)
-    if torch.cuda.current_device() == device.index:
-        return call(*args, _raw_stream(None, device))
-    with torch.cuda.device(device):
-        return call(*args, _raw_stream(None, device))
+    if stream is None:
+        if torch.cuda.current_device() == device.index:
+            return call(*args, _raw_stream(None, device))
+        with torch.cuda.device(device):
+            return call(*args, _raw_stream(None, device))
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the layer on {device}")
+    with torch.cuda.stream(stream):           # makes the stream's device current as well
+        return call(*args, stream.cuda_stream)
 
 
 class FP8Linear:
@@ -478,19 +478,18 @@ class RotaryND:
         return _on(self.device, stream, self._call, q, k, pos, q_out, k_out, inverse)
 
     def _call(self, q, k, pos, q_out, k_out, inverse, s):
-        device = self.device
-        if q.dim() != 3 or pos.dim() != 2 or pos.shape[0] != q.shape[0]:
-            raise ValueError(f"RotaryND: q must be [M, heads, {self.D}] and pos [M, {self.axes}], got "
-                             f"{tuple(q.shape)} and {tuple(pos.shape)}")
         if k is None and k_out is not None:
             raise ValueError("RotaryND: k_out without k")
-        for t in (q, k, pos, q_out, k_out):
-            if t is not None and t.device != device:
-                raise ValueError(f"RotaryND: every tensor must be on {device}, got {t.device}")
+        if q.dim() != 3 or pos.dim() != 2 or (k is not None and k.dim() != 3):
+            raise ValueError(f"RotaryND: q and k must be [M, heads, {self.D}] and pos [M, {self.axes}]")
         if q_out is None:
             q_out = q.new_empty(q.shape)
         if k_out is None and k is not None:
             k_out = k.new_empty(k.shape)
+        index = self.device.index
+        for t in (q, pos, q_out) if k is None else (q, k, pos, q_out, k_out):
+            if t.get_device() != index:
+                raise ValueError(f"RotaryND: every tensor must be on {self.device}, got {t.device}")
         lib.rope_nd(q, k, self.plan, pos, q_out, k_out, self.q_norm, None if k is None else self.k_norm, inverse,
                     self.eps, s)
         return q_out, k_out

@@ -192,8 +192,6 @@ def _need_2d(t, rows, cols, name):
 
 def _stream(stream):
     import torch
-    if isinstance(stream, int):     # a raw handle
-        return stream
     s = stream if stream is not None else torch.cuda.current_stream()
     return ctypes.c_void_p(s.cuda_stream)
 
@@ -774,17 +772,15 @@ def fp8_linear_grouped(X, offsets, packed, bias, N, epilogue, gelu_col_begin, Y,
         _fp8_workspace(workspace, M, K, E), _stream(stream)))
 
 
-def _rope_tensor(x, y, norm, M, D, name):
+def _rope_tensor(x, y, norm, M, D, dtype, name):
     """Checks one tensor's heads [M, heads, D] and returns its packed rope_nd_tensor."""
-    import torch
     shape = x.shape
     if len(shape) != 3 or shape[0] != M or shape[2] != D or y.shape != shape:
         raise ValueError(f"{name} must be [{M}, heads, {D}] and its output alike, got {tuple(x.shape)} and "
                          f"{tuple(y.shape)}")
-    if x.dtype is not torch.bfloat16 or y.dtype is not torch.bfloat16:
-        raise ValueError(f"{name} must have dtype {torch.bfloat16}, got {x.dtype} and {y.dtype}")
-    if not (x.is_cuda and y.is_cuda):
-        raise ValueError(f"{name} must be a CUDA tensor")
+    if x.dtype is not dtype or y.dtype is not dtype or not (x.is_cuda and y.is_cuda):
+        raise ValueError(f"{name} and its output must be {dtype} CUDA tensors, got {x.dtype} on {x.device} and "
+                         f"{y.dtype} on {y.device}")
     H = shape[1]
     (xr, xh, xd), (yr, yh, yd) = x.stride(), y.stride()
     if xd != 1 or yd != 1:
@@ -793,29 +789,27 @@ def _rope_tensor(x, y, norm, M, D, name):
         xr = yr = 0
     if H <= 1:
         xh = yh = 0
-    return ROPE_TENSOR.pack(x.data_ptr(), xr, xh, y.data_ptr(), yr, yh, 0 if norm is None else norm.data_ptr(), H)
+    if norm is None:
+        return ROPE_TENSOR.pack(x.data_ptr(), xr, xh, y.data_ptr(), yr, yh, 0, H)
+    if norm.dtype is not dtype or norm.numel() != D or not norm.is_contiguous() or not norm.is_cuda:
+        raise ValueError(f"a norm weight must be {dtype} CUDA [{D}]")
+    return ROPE_TENSOR.pack(x.data_ptr(), xr, xh, y.data_ptr(), yr, yh, norm.data_ptr(), H)
 
 
 def rope_nd(q, k, plan, pos, q_out, k_out, q_norm=None, k_norm=None, inverse=False, eps=1e-6, stream=None):
     """Enqueues the rotary positions of q [M, heads, D] and k (likewise, or None), bf16 CUDA, into q_out and
     k_out (which may be q and k).  pos: int32 or float32 CUDA [M, axes]; norms: bf16 CUDA [D] or None."""
     import torch
-    D, axes = plan.D, plan.axes
-    if pos.dim() != 2 or pos.shape[1] != axes or (axes > 1 and pos.stride(1) != 1):
-        raise ValueError(f"pos must be [M, {axes}] with unit stride in its last dimension, got {tuple(pos.shape)}")
-    if pos.dtype is not torch.int32 and pos.dtype is not torch.float32:
-        raise ValueError(f"pos must be int32 or float32, got {pos.dtype}")
-    if not pos.is_cuda:
-        raise ValueError("pos must be a CUDA tensor")
-    for norm in (q_norm, k_norm):
-        if norm is not None and (norm.dtype is not torch.bfloat16 or norm.numel() != D or not norm.is_contiguous()
-                                 or not norm.is_cuda):
-            raise ValueError(f"a norm weight must be bf16 CUDA [{D}]")
-    M = pos.shape[0]
-    tq = _rope_tensor(q, q_out, q_norm, M, D, "q")
-    tk = None if k is None else _rope_tensor(k, k_out, k_norm, M, D, "k")
-    rc = load().rope_nd(tq, tk, M, plan, pos.data_ptr(), pos.stride(0) if M > 1 else 0, pos.dtype is torch.float32,
-                        inverse, eps, _stream(stream))
+    shape, kind = pos.shape, pos.dtype
+    if len(shape) != 2 or shape[1] != plan.axes or (plan.axes > 1 and pos.stride(1) != 1):
+        raise ValueError(f"pos must be [M, {plan.axes}] with unit stride in its last dimension, got {tuple(shape)}")
+    if (kind is not torch.int32 and kind is not torch.float32) or not pos.is_cuda:
+        raise ValueError(f"pos must be an int32 or float32 CUDA tensor, got {kind} on {pos.device}")
+    M = shape[0]
+    tq = _rope_tensor(q, q_out, q_norm, M, plan.D, torch.bfloat16, "q")
+    tk = None if k is None else _rope_tensor(k, k_out, k_norm, M, plan.D, torch.bfloat16, "k")
+    rc = load().rope_nd(tq, tk, M, plan, pos.data_ptr(), pos.stride(0) if M > 1 else 0, kind is torch.float32,
+                        inverse, eps, stream if type(stream) is int else _stream(stream))
     if rc != OK:
         _check("rope_nd", rc)
 
