@@ -39,8 +39,8 @@ int run(const char *fn, const void *X, int M, int K, int ldx, const int *offsets
   if (!X || !packed || !Y) return fail(SVDQ_ERR_INVALID_ARG, name + ": null pointer");
   if (epilogue < SVDQ_EPILOGUE_NONE || epilogue > SVDQ_EPILOGUE_GELU_TANH)
     return fail(SVDQ_ERR_INVALID_ARG, name + ": unknown epilogue");
-  if (M < 1 || K < 8 || K % 8 || N < 8 || N % 8 || ldx < K || ldx % 8 || ldy < N || ldy % 8)
-    return fail(SVDQ_ERR_SHAPE, name + ": need M >= 1, K % 8 == 0, N % 8 == 0, ldx >= K, ldy >= N, ldx % 8 == 0, "
+  if (M < 1 || M > FP8_MAX_ROWS || K < 8 || K % 8 || N < 8 || N % 8 || ldx < K || ldx % 8 || ldy < N || ldy % 8)
+    return fail(SVDQ_ERR_SHAPE, name + ": need 1 <= M <= 2^30, K % 8 == 0, N % 8 == 0, ldx >= K, ldy >= N, ldx % 8 == 0, "
                                        "ldy % 8 == 0");
   if (experts < 1 || experts > FP8_MAX_EXPERTS) return fail(SVDQ_ERR_SHAPE, name + ": need 1 <= experts <= 512");
   if (gelu_col_begin < 0 || gelu_col_begin > N) return fail(SVDQ_ERR_SHAPE, name + ": gelu_col_begin outside [0, N]");

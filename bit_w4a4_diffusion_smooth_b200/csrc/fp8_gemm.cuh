@@ -95,28 +95,32 @@ __device__ __forceinline__ float2 gelu_tanh2(float2 y) {
   return make_float2(y.x * dev::rcp_approx_ftz(1.0f + dev::ex2_approx_ftz(z.x)),
                      y.y * dev::rcp_approx_ftz(1.0f + dev::ex2_approx_ftz(z.y)));
 }
-// GELU, erf form, of two values, with one special-function instruction each: 0.5 y (1 + erf x), x = y / sqrt 2.
-// erf by Abramowitz & Stegun, Handbook of Mathematical Functions, formula 7.1.28: for x >= 0
-// 1 - erf x = (1 + a1 x + ... + a6 x^6)^-16 = q, |error| <= 3e-7; 1 + erf x is 2 - q for x >= 0 and q(|x|) below,
-// taken directly, without cancellation.  (The formula with an exponential takes two such instructions, which
-// bound the epilogue: 56 pairs a lane and half tile.)  The polynomial overflows to infinity only where q is 0.
+// GELU, erf form, of two values: y Phi(y) = max(y, 0) - |y| Phi(-|y|), without cancellation on either side.
+// Phi(-a) = (1 - erf(a / sqrt 2)) / 2 by Abramowitz & Stegun, Handbook of Mathematical Functions, formula 7.1.28:
+// 1 - erf x = (1 + a1 x + ... + a6 x^6)^-16 for x >= 0, |error| <= 3e-7.  The coefficients below are
+// 2^(1/16) a_i 2^(-i/2) (-1)^i: the half, the root and the sign of -a are in them.  One special-function
+// instruction a value (the formula with an exponential takes two) and 17 instructions a pair: under load the
+// epilogue's instructions cost power that the MMAs then lack.  a is capped at 20, where Phi(-a) is 0 in float32;
+// the maximum passes NaN on.
+__device__ __forceinline__ float max0_nan(float y) {
+  float r;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(y));
+  return r;
+}
 __device__ __forceinline__ float2 gelu_erf2_rcp(float2 y) {
-  const float2 x = dev::mul2_rn(y, make_float2(0.70710678118654752f, 0.70710678118654752f));
-  const float2 ax = make_float2(fabsf(x.x), fabsf(x.y));
-  float2 d = dev::fma2_rn(make_float2(0.0000430638f, 0.0000430638f), ax, make_float2(0.0002765672f, 0.0002765672f));
-  d = dev::fma2_rn(d, ax, make_float2(0.0001520143f, 0.0001520143f));
-  d = dev::fma2_rn(d, ax, make_float2(0.0092705272f, 0.0092705272f));
-  d = dev::fma2_rn(d, ax, make_float2(0.0422820123f, 0.0422820123f));
-  d = dev::fma2_rn(d, ax, make_float2(0.0705230784f, 0.0705230784f));
-  d = dev::fma2_rn(d, ax, make_float2(1.0f, 1.0f));
+  const float2 na = make_float2(fmaxf(-fabsf(y.x), -20.0f), fmaxf(-fabsf(y.y), -20.0f));
+  float2 d = dev::fma2_rn(make_float2(5.62129966e-06f, 5.62129966e-06f), na, make_float2(-5.1055209e-05f, -5.1055209e-05f));
+  d = dev::fma2_rn(d, na, make_float2(3.9686137e-05f, 3.9686137e-05f));
+  d = dev::fma2_rn(d, na, make_float2(-0.00342273924f, -0.00342273924f));
+  d = dev::fma2_rn(d, na, make_float2(0.0220769985f, 0.0220769985f));
+  d = dev::fma2_rn(d, na, make_float2(-0.052075163f, -0.052075163f));
+  d = dev::fma2_rn(d, na, make_float2(1.04427378f, 1.04427378f));
   float2 q = make_float2(dev::rcp_approx_ftz(d.x), dev::rcp_approx_ftz(d.y));
   q = dev::mul2_rn(q, q);
   q = dev::mul2_rn(q, q);
   q = dev::mul2_rn(q, q);
   q = dev::mul2_rn(q, q);
-  const float2 r = dev::fma2_rn(make_float2(-1.0f, -1.0f), q, make_float2(2.0f, 2.0f));
-  const float2 one_plus_erf = make_float2(x.x >= 0.0f ? r.x : q.x, x.y >= 0.0f ? r.y : q.y);
-  return dev::mul2_rn(dev::mul2_rn(y, make_float2(0.5f, 0.5f)), one_plus_erf);
+  return dev::fma2_rn(na, q, make_float2(max0_nan(y.x), max0_nan(y.y)));
 }
 template <int EPI>
 __device__ __forceinline__ float2 activate2(float2 y) {

@@ -129,8 +129,8 @@ extern "C" int fp8_weight_size(int K, int N, int experts, size_t *bytes) {
 
 extern "C" int fp8_workspace_size(int M, int K, int experts, size_t *bytes) {
   if (!bytes) return fail(SVDQ_ERR_INVALID_ARG, "fp8_workspace_size: null pointer");
-  if (M < 1 || K < 8 || K % 8 || experts < 1 || experts > FP8_MAX_EXPERTS)
-    return fail(SVDQ_ERR_SHAPE, "fp8_workspace_size: need M >= 1, K % 8 == 0, 1 <= experts <= 512");
+  if (M < 1 || M > FP8_MAX_ROWS || K < 8 || K % 8 || experts < 1 || experts > FP8_MAX_EXPERTS)
+    return fail(SVDQ_ERR_SHAPE, "fp8_workspace_size: need 1 <= M <= 2^30, K % 8 == 0, 1 <= experts <= 512");
   *bytes = fp8::needs_workspace(M, experts) ? fp8::act_bytes(M, K) : 0;
   return ok();
 }

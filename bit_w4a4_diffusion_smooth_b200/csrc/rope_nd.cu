@@ -271,10 +271,10 @@ extern "C" int rope_nd(const rope_nd_tensor_t *Q, const rope_nd_tensor_t *K, int
   if (plan->pairing != ROPE_ND_INTERLEAVED && plan->pairing != ROPE_ND_HALF)
     return fail(SVDQ_ERR_INVALID_ARG, "rope_nd: unknown pairing");
   const int D = plan->D;
-  if (M < 1 || D < 8 || D > MAX_D || D % 8 || plan->axes < 1 || plan->axes > D / 2 || Q->heads < 1 ||
+  if (M < 1 || M > ROPE_ND_MAX_ROWS || D < 8 || D > MAX_D || D % 8 || plan->axes < 1 || plan->axes > D / 2 || Q->heads < 1 ||
       (K && K->heads < 1) || pos_row < 0 ||
       Q->heads > 65535 || (K && K->heads > 65535))
-    return fail(SVDQ_ERR_SHAPE, "rope_nd: need M >= 1, D % 8 == 0, 8 <= D <= 256, 1 <= axes <= D / 2, 1 <= heads <= "
+    return fail(SVDQ_ERR_SHAPE, "rope_nd: need 1 <= M <= 2^30, D % 8 == 0, 8 <= D <= 256, 1 <= axes <= D / 2, 1 <= heads <= "
                                 "65535, pos_row >= 0");
   Params p{};
   for (int i = 0; i < D / 2; ++i) {

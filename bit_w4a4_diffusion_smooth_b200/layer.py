@@ -396,7 +396,7 @@ class FP8Linear:
             raise ValueError(f"{name}: X must have unit stride in its last dimension")
         M, ldy = shape[0], N
         if Y is None:
-            Y = X.new_empty((M, N)) if offsets is None else X.new_zeros((M, N))
+            Y = X.new_empty(M, N) if offsets is None else X.new_zeros((M, N))
         else:
             _check_output(Y, M, N, self.device, name)
             ldy, step = Y.stride()
@@ -404,6 +404,8 @@ class FP8Linear:
                 raise ValueError(f"{name}: Y must have unit stride in its last dimension")
         if M == 1:                                # a single row's stride is its width, whatever torch recorded
             ldx, ldy = K, N
+        elif M >= 2 ** 31 or ldx >= 2 ** 31 or ldy >= 2 ** 31:
+            raise ValueError(f"{name}: X or Y is too large")   # a C int would cut these down without a word
         experts = self.experts or 1
         need = lib.fp8_workspace_size(M, K, experts)
         ws = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
@@ -483,9 +485,9 @@ class RotaryND:
         if q.dim() != 3 or pos.dim() != 2 or (k is not None and k.dim() != 3):
             raise ValueError(f"RotaryND: q and k must be [M, heads, {self.D}] and pos [M, {self.axes}]")
         if q_out is None:
-            q_out = q.new_empty(q.shape)
+            q_out = torch.empty_like(q)
         if k_out is None and k is not None:
-            k_out = k.new_empty(k.shape)
+            k_out = torch.empty_like(k)
         index = self.device.index
         for t in (q, pos, q_out) if k is None else (q, k, pos, q_out, k_out):
             if t.get_device() != index:

@@ -708,8 +708,16 @@ def fp8_workspace_size(M, K, experts=1):
 
 
 def _row_stride(t, cols):
-    """Row stride of a 2-D tensor; a single row's is its width, whatever torch recorded for it."""
-    return t.stride(0) if t.shape[0] != 1 else cols
+    """Row stride of a 2-D tensor as the C int it is passed as; a single row's is its width, whatever torch
+    recorded for it."""
+    return _c_int(t.stride(0), "a row stride") if t.shape[0] != 1 else cols
+
+
+def _c_int(v, name):
+    """`v`, if a C int holds it (ctypes would cut it down without a word)."""
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise ValueError(f"{name} of {v} is too large")
+    return v
 
 
 def fp8_pack_weights(W, packed=None, stream=None):
@@ -718,14 +726,14 @@ def fp8_pack_weights(W, packed=None, stream=None):
     import torch
     if W.dim() not in (2, 3):
         raise ValueError(f"W must be [K, N] or [experts, K, N], got {tuple(W.shape)}")
-    E, K, N = (1, *W.shape) if W.dim() == 2 else W.shape
+    E, K, N = (_c_int(n, "a dimension of W") for n in ((1, *W.shape) if W.dim() == 2 else W.shape))
     need = fp8_weight_size(K, N, E)
     p = _dptr(W, "W", torch.bfloat16)
     if packed is None:
         packed = torch.empty(need, dtype=torch.uint8, device=W.device)
     _need_bytes(packed, need, "packed")
     _check("fp8_pack_weights", load().fp8_pack_weights(
-        p, K, N, W.stride(-2), W.stride(0) if E > 1 else 0, E, _dptr(packed, "packed", torch.uint8), _stream(stream)))
+        p, K, N, _c_int(W.stride(-2), "W's row stride"), W.stride(0) if E > 1 else 0, E, _dptr(packed, "packed", torch.uint8), _stream(stream)))
     return packed
 
 
@@ -744,7 +752,7 @@ def _fp8_workspace(workspace, M, K, experts):
 def fp8_linear(X, packed, bias, N, epilogue, gelu_col_begin, Y, workspace=None, stream=None):
     """Enqueues the FP8 linear layer.  X: bf16 CUDA [M, K]; Y: bf16 CUDA [M, N] (row strides ldx, ldy)."""
     import torch
-    M, K = X.shape
+    M, K = (_c_int(n, "a dimension of X") for n in X.shape)
     _need_bytes(packed, fp8_weight_size(K, N), "packed")
     _need_bytes(bias, 2 * N, "bias")
     _need_2d(Y, M, N, "Y")
@@ -758,8 +766,8 @@ def fp8_linear_grouped(X, offsets, packed, bias, N, epilogue, gelu_col_begin, Y,
     """Enqueues the FP8 product by expert.  X: bf16 CUDA [M, K]; offsets: int32 CUDA [experts + 1]; bias: bf16
     CUDA [experts, N] or None; Y: bf16 CUDA [M, N]."""
     import torch
-    M, K = X.shape
-    E = offsets.numel() - 1
+    M, K = (_c_int(n, "a dimension of X") for n in X.shape)
+    E = _c_int(offsets.numel() - 1, "the number of experts")
     _need_bytes(packed, fp8_weight_size(K, N, E), "packed")
     _need_bytes(bias, 2 * N * E, "bias")
     _need_2d(Y, M, N, "Y")
@@ -805,7 +813,7 @@ def rope_nd(q, k, plan, pos, q_out, k_out, q_norm=None, k_norm=None, inverse=Fal
         raise ValueError(f"pos must be [M, {plan.axes}] with unit stride in its last dimension, got {tuple(shape)}")
     if (kind is not torch.int32 and kind is not torch.float32) or not pos.is_cuda:
         raise ValueError(f"pos must be an int32 or float32 CUDA tensor, got {kind} on {pos.device}")
-    M = shape[0]
+    M = _c_int(shape[0], "the number of rows")
     tq = _rope_tensor(q, q_out, q_norm, M, plan.D, torch.bfloat16, "q")
     tk = None if k is None else _rope_tensor(k, k_out, k_norm, M, plan.D, torch.bfloat16, "k")
     rc = load().rope_nd(tq, tk, M, plan, pos.data_ptr(), pos.stride(0) if M > 1 else 0, kind is torch.float32,

@@ -550,6 +550,7 @@ int svdq_linear_int4(const uint8_t *a_codes, const void *a_scales, const void *U
  * no infinity): the row (of X) or column (of W) that holds it gives NaN.
  */
 #define FP8_MAX_EXPERTS 512
+#define FP8_MAX_ROWS (1 << 30)
 
 /* Bytes of a packed weight: `experts` matrices of K x N (1 for fp8_linear).
  * Rules: K >= 8, K % 8 == 0, N >= 8, N % 8 == 0, 1 <= experts <= FP8_MAX_EXPERTS. */
@@ -576,8 +577,8 @@ int fp8_pack_weights(const void *W, int K, int N, int ldw, int64_t expert_stride
  * workspace: fp8_workspace_size(M, K, experts) bytes (NULL where that is 0), in
  * use until the call has run on the stream (calls that may overlap take
  * workspaces of their own).
- * Rules: M >= 1, K >= 8, K % 8 == 0, ldx >= K, ldx % 8 == 0, N >= 8, N % 8 == 0,
- * ldy >= N, ldy % 8 == 0, 0 <= gelu_col_begin <= N.
+ * Rules: 1 <= M <= FP8_MAX_ROWS, K >= 8, K % 8 == 0, ldx >= K, ldx % 8 == 0,
+ * N >= 8, N % 8 == 0, ldy >= N, ldy % 8 == 0, 0 <= gelu_col_begin <= N.
  */
 int fp8_linear(const void *X, int M, int K, int ldx, const void *packed, const void *bias, int N, int epilogue,
                int gelu_col_begin, void *Y, int ldy, void *workspace, svdq_stream_t stream);
@@ -609,6 +610,7 @@ enum rope_nd_pairing {
   ROPE_ND_INTERLEAVED = 0,        /* pair i: elements 2i and 2i + 1 of the head */
   ROPE_ND_HALF = 1                /* pair i: elements i and i + D/2 */
 };
+#define ROPE_ND_MAX_ROWS (1 << 30)
 /* What the pairs of a head turn by (a HOST structure, read during the call). */
 typedef struct rope_nd_plan {
   int D;                          /* head dimension */
@@ -631,7 +633,7 @@ typedef struct rope_nd_tensor {
  * pos: M rows of `axes` values, pos_row elements apart: int32, or float32 with
  * pos_is_float.  inverse: by the negated angle (undoes a turn; also the turn's
  * gradient); not with a norm.
- * Rules: M >= 1; 8 <= D <= 256, D % 8 == 0; 1 <= axes <= D/2; axis[i] < axes;
+ * Rules: 1 <= M <= ROPE_ND_MAX_ROWS; 8 <= D <= 256, D % 8 == 0; 1 <= axes <= D/2; axis[i] < axes;
  * 1 <= heads <= 65535; strides multiples of 8; pointers 16-byte aligned (pos
  * 4-byte); pos_row >= 0 (0: one position for all rows); the heads of a Y must
  * not overlap one another.

@@ -22,7 +22,7 @@ def test_sizes():
         with pytest.raises(lib.SvdqError) as e:
             lib.fp8_weight_size(*bad)
         assert e.value.status == lib.ERR_SHAPE
-    for bad in ((0, 8), (1, 4), (1, 0), (-1, 8), (4, 8, 0), (4, 8, 513)):
+    for bad in ((0, 8), (1, 4), (1, 0), (-1, 8), (2 ** 30 + 1, 8), (4, 8, 0), (4, 8, 513)):
         with pytest.raises(lib.SvdqError) as e:
             lib.fp8_workspace_size(*bad)
         assert e.value.status == lib.ERR_SHAPE
@@ -35,7 +35,7 @@ def _linear(x=P, M=4, K=64, ldx=64, w=P, bias=None, N=64, epi=0, begin=0, y=P, l
 @pytest.mark.parametrize("kw,want", [
     (dict(x=None), lib.ERR_INVALID_ARG), (dict(w=None), lib.ERR_INVALID_ARG), (dict(y=None), lib.ERR_INVALID_ARG),
     (dict(M=129, ws=None), lib.ERR_INVALID_ARG), (dict(epi=3), lib.ERR_INVALID_ARG), (dict(epi=-1), lib.ERR_INVALID_ARG),
-    (dict(M=0), lib.ERR_SHAPE), (dict(M=-5), lib.ERR_SHAPE), (dict(K=60), lib.ERR_SHAPE), (dict(K=0), lib.ERR_SHAPE),
+    (dict(M=0), lib.ERR_SHAPE), (dict(M=-5), lib.ERR_SHAPE), (dict(M=2 ** 30 + 1), lib.ERR_SHAPE), (dict(K=60), lib.ERR_SHAPE), (dict(K=0), lib.ERR_SHAPE),
     (dict(N=60), lib.ERR_SHAPE), (dict(N=0), lib.ERR_SHAPE), (dict(ldx=56), lib.ERR_SHAPE), (dict(ldx=68), lib.ERR_SHAPE),
     (dict(ldy=56), lib.ERR_SHAPE), (dict(ldy=68), lib.ERR_SHAPE), (dict(begin=-1), lib.ERR_SHAPE),
     (dict(begin=65), lib.ERR_SHAPE), (dict(M=2 ** 31 - 1, N=2 ** 20, ldy=2 ** 20), lib.ERR_SHAPE),
@@ -71,7 +71,7 @@ def _rope(q=None, k=None, M=4, plan=None, pos=P, row=2, inverse=0):
 
 
 @pytest.mark.parametrize("kw,want", [
-    (dict(pos=None), lib.ERR_INVALID_ARG), (dict(M=0), lib.ERR_SHAPE), (dict(row=-1), lib.ERR_SHAPE),
+    (dict(pos=None), lib.ERR_INVALID_ARG), (dict(M=0), lib.ERR_SHAPE), (dict(M=2 ** 30 + 1), lib.ERR_SHAPE), (dict(row=-1), lib.ERR_SHAPE),
     (dict(plan=_plan(pairing=2)), lib.ERR_INVALID_ARG), (dict(plan=_plan(D=12)), lib.ERR_SHAPE),
     (dict(plan=_plan(D=264)), lib.ERR_SHAPE), (dict(plan=_plan(D=0)), lib.ERR_SHAPE), (dict(plan=_plan(axes=0)), lib.ERR_SHAPE),
     (dict(plan=_plan(axes=9)), lib.ERR_SHAPE), (dict(pos=ctypes.c_void_p(18)), lib.ERR_ALIGNMENT),
@@ -106,3 +106,14 @@ def test_layers_refuse_host_tensors_and_bad_shapes():
                  lambda: layer.RotaryND([4]), lambda: layer.RotaryND([200, 64]), lambda: layer.RotaryND([16], theta=0)):
         with pytest.raises(ValueError):
             make()
+
+
+def test_sizes_past_a_c_int_are_refused_not_cut_down():
+    """2^32 + 4 rows would arrive as 4."""
+    far = torch.empty_strided((2, 64), (2 ** 31, 1), dtype=torch.bfloat16, device="meta")
+    with pytest.raises(ValueError):
+        lib._row_stride(far, 64)
+    for n in (2 ** 31, 2 ** 32 + 4, -2 ** 31 - 1):
+        with pytest.raises(ValueError):
+            lib._c_int(n, "rows")
+    assert lib._c_int(2 ** 31 - 1, "rows") == 2 ** 31 - 1

@@ -158,6 +158,20 @@ def test_non_finite_rows_and_columns_stay_their_own():
     assert (np.abs(got - y) <= 2.0 ** -8 * np.abs(y) + 2 * K * 2.0 ** -23 * mag)[keep].all()
 
 
+@pytest.mark.parametrize("M,N", [(9, 200), (100, 200), (2600, 5640)])
+@pytest.mark.parametrize("epilogue", EPI[1:])
+def test_gelu_passes_nan_on_and_settles_far_out(M, N, epilogue):
+    """NaN rows stay NaN through the GELUs; far out they are the value itself and zero."""
+    K = 136
+    x, w = np.zeros((M, K)), np.zeros((K, N))
+    x[:, 0], w[0, 0::2], w[0, 1::2] = 64.0, 4.0, -4.0         # 256 and -256
+    x[M - 1, 5] = np.nan
+    Y, _ = run_linear(x, w, None, epilogue)
+    got = G.bf16_host(Y)
+    assert np.isnan(got[M - 1]).all()
+    assert (got[:M - 1, 0::2] == 256).all() and (got[:M - 1, 1::2] == 0).all()
+
+
 def test_zero_rows_give_the_bias():
     K, N = 256, 136
     w, b = rand(2, K, N, loud=False), rand(3, N, loud=False)
