@@ -16,7 +16,9 @@ namespace fp8 {
 namespace {
 
 // One warp per (row, scale word): 512 elements, 16 per lane, so 8 lanes hold a
-// block of 128.  Two 16-byte loads and one 16-byte store per lane.
+// block of 128.  Two 16-byte loads and one 16-byte store per lane.  The place
+// in the sequence moves by increments: its division had been half of the
+// kernel's instructions (4608 x 2560: 7.7 us, 68% of issue slots).
 constexpr int QUANT_THREADS = 256;
 
 __global__ void __launch_bounds__(QUANT_THREADS)
@@ -25,11 +27,15 @@ __global__ void __launch_bounds__(QUANT_THREADS)
   dev::grid_dependency_wait();
   dev::grid_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const long long warps = static_cast<long long>(gridDim.x) * (QUANT_THREADS / 32);
-  const long long total = static_cast<long long>(M) * KW;
-  for (long long it = static_cast<long long>(blockIdx.x) * (QUANT_THREADS / 32) + (threadIdx.x >> 5); it < total;
-       it += warps) {
-    const int row = static_cast<int>(it / KW), kw = static_cast<int>(it % KW);
+  const int warps = static_cast<int>(gridDim.x) * (QUANT_THREADS / 32);
+  const int at = static_cast<int>(blockIdx.x) * (QUANT_THREADS / 32) + static_cast<int>(threadIdx.x >> 5);
+  const int rows_on = warps / KW, words_on = warps % KW;
+  int row = at / KW, kw = at % KW;
+  for (; row < M; row += rows_on, kw += words_on) {
+    if (kw >= KW) {
+      kw -= KW;
+      if (++row >= M) break;
+    }
     const int k0 = kw * 512 + lane * 16;
     const uint16_t *src = X + static_cast<size_t>(row) * ldx + k0;
     uint4 v[2];

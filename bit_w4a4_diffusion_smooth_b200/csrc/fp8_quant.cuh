@@ -69,20 +69,17 @@ __device__ __forceinline__ uint32_t quantize16(const uint32_t (&w)[8], uint32_t 
   }
   const uint32_t byte = scale_byte(top << 16);
   const float inv = inverse_scale(byte);
+  const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float f[4];
+    float2 f[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      f[2 * j] = __uint_as_float(w[2 * i + j] << 16);
-      f[2 * j + 1] = __uint_as_float(w[2 * i + j] & 0xFFFF0000u);
+      f[j] = make_float2(__uint_as_float(w[2 * i + j] << 16), __uint_as_float(w[2 * i + j] & 0xFFFF0000u));
+      if (odd) f[j] = make_float2(nan_if_infinite(f[j].x), nan_if_infinite(f[j].y));
+      f[j] = dev::mul2_rn(f[j], inv2);
     }
-    if (odd) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) f[j] = nan_if_infinite(f[j]);
-    }
-    out[i] = cvt_e4m3x2(__fmul_rn(f[0], inv), __fmul_rn(f[1], inv)) |
-             (cvt_e4m3x2(__fmul_rn(f[2], inv), __fmul_rn(f[3], inv)) << 16);
+    out[i] = cvt_e4m3x2(f[0].x, f[0].y) | (cvt_e4m3x2(f[1].x, f[1].y) << 16);
   }
   return byte;
 }
