@@ -330,14 +330,21 @@ class AWQLinear:
         return Y
 
 
+# The caller's current device and its current stream's handle; torch's public functions for them take several times
+# as long, which shows in calls whose GPU time is a few microseconds.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
 def _on(device, stream, call, *args):
     """call(*args, raw stream) with `device` current and torch allocating on the stream the work runs on: `stream`,
     else the caller's current stream of that device."""
+    index = device.index
     if stream is None:
-        if torch.cuda.current_device() == device.index:
-            return call(*args, _raw_stream(None, device))
+        if _current_device() == index:
+            return call(*args, _current_stream(index))
         with torch.cuda.device(device):
-            return call(*args, _raw_stream(None, device))
+            return call(*args, _current_stream(index))
     if stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the layer on {device}")
     with torch.cuda.stream(stream):           # makes the stream's device current as well
@@ -385,27 +392,24 @@ class FP8Linear:
 
     def _call(self, X, offsets, Y, s):
         """The checked call on raw stream `s`, which torch allocates on."""
-        name = type(self).__name__
         shape, K, N = X.shape, self.K, self.N
-        if len(shape) != 2 or shape[1] != K:
-            raise ValueError(f"{name}: X must be [M, {K}], got {tuple(shape)}")
-        if X.dtype is not torch.bfloat16 or X.device != self.device:
-            raise ValueError(f"{name}: X must be bf16 on {self.device}, got {X.dtype} on {X.device}")
+        if len(shape) != 2 or shape[1] != K or X.dtype is not torch.bfloat16 or X.get_device() != self.device.index:
+            _check_input(X, K, self.device, type(self).__name__)   # says which
+        M = shape[0]
         ldx, step = X.stride()
-        if step != 1:
-            raise ValueError(f"{name}: X must have unit stride in its last dimension")
-        M, ldy = shape[0], N
         if Y is None:
-            Y = X.new_empty(M, N) if offsets is None else X.new_zeros((M, N))
+            Y, ldy = (X.new_empty(M, N) if offsets is None else X.new_zeros((M, N))), N
         else:
-            _check_output(Y, M, N, self.device, name)
-            ldy, step = Y.stride()
-            if step != 1:
-                raise ValueError(f"{name}: Y must have unit stride in its last dimension")
+            _check_output(Y, M, N, self.device, type(self).__name__)
+            ldy, y_step = Y.stride()
+            step = step if y_step == 1 else 0
+        if step != 1:
+            raise ValueError(f"{type(self).__name__}: X and Y must have unit stride in their last dimension")
         if M == 1:                                # a single row's stride is its width, whatever torch recorded
             ldx, ldy = K, N
         elif M >= 2 ** 31 or ldx >= 2 ** 31 or ldy >= 2 ** 31:
-            raise ValueError(f"{name}: X or Y is too large")   # a C int would cut these down without a word
+            # a C int would cut these down without a word
+            raise ValueError(f"{type(self).__name__}: X or Y is too large")
         experts = self.experts or 1
         need = lib.fp8_workspace_size(M, K, experts)
         ws = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
