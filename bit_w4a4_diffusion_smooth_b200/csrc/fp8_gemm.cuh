@@ -83,6 +83,15 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
       : "r"(taddr));
 }
 
+// Two float32 sums (one packed instruction).
+__device__ __forceinline__ float2 add2_rn(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<const uint64_t *>(&a)), "l"(*reinterpret_cast<const uint64_t *>(&b)));
+  return *reinterpret_cast<const float2 *>(&r);
+}
+
 // GELU, tanh form, of two values: 0.5 y (1 + tanh z) = y / (1 + exp(-2 z)), z = sqrt(2/pi) (y + 0.044715 y^3):
 // no cancellation for negative y, and exp and the reciprocal come from the hardware approximations (a few
 // 1e-7 relative), far below the bf16 rounding of the result.  exp(-2 z) overflows to infinity only where the
@@ -92,8 +101,8 @@ __device__ __forceinline__ float2 gelu_tanh2(float2 y) {
   // -2 z log2(e) = y (c0 + c1 y^2), c0 = -2 sqrt(2/pi) log2(e), c1 = 0.044715 c0
   const float2 p = dev::fma2_rn(make_float2(-0.10294324f, -0.10294324f), y2, make_float2(-2.3022082f, -2.3022082f));
   const float2 z = dev::mul2_rn(y, p);
-  return make_float2(y.x * dev::rcp_approx_ftz(1.0f + dev::ex2_approx_ftz(z.x)),
-                     y.y * dev::rcp_approx_ftz(1.0f + dev::ex2_approx_ftz(z.y)));
+  const float2 e = add2_rn(make_float2(dev::ex2_approx_ftz(z.x), dev::ex2_approx_ftz(z.y)), make_float2(1.0f, 1.0f));
+  return dev::mul2_rn(y, make_float2(dev::rcp_approx_ftz(e.x), dev::rcp_approx_ftz(e.y)));
 }
 // GELU, erf form, of two values: y Phi(y) = max(y, 0) - |y| Phi(-|y|), without cancellation on either side.
 // Phi(-a) = (1 - erf(a / sqrt 2)) / 2 by Abramowitz & Stegun, Handbook of Mathematical Functions, formula 7.1.28:

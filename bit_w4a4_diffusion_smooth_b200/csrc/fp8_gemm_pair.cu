@@ -101,15 +101,19 @@ __device__ __forceinline__ void abort_pair(volatile int *abort_flag, uint32_t pe
   dev::report(status, SVDQ_ERR_TIMEOUT);
 }
 
-// Bias (16 bf16), activation and rounding of 16 columns, the GELU from column `act` of the 16 on.
+// Bias (16 bf16, if there is one), activation and rounding of 16 columns, the GELU from column `act` of the 16 on.
 template <int EPI>
-__device__ __forceinline__ void finish16(const uint32_t (&v)[16], const uint4 (&bb)[2], int act, uint32_t (&out)[8]) {
-  const uint32_t bw[8] = {bb[0].x, bb[0].y, bb[0].z, bb[0].w, bb[1].x, bb[1].y, bb[1].z, bb[1].w};
+__device__ __forceinline__ void finish16(const uint32_t (&v)[16], bool biased, const uint4 (&bb)[2], int act,
+                                         uint32_t (&out)[8]) {
   float2 t[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    t[j] = make_float2(__uint_as_float(v[2 * j]) + __uint_as_float(bw[j] << 16),
-                       __uint_as_float(v[2 * j + 1]) + __uint_as_float(bw[j] & 0xFFFF0000u));
+  for (int j = 0; j < 8; ++j) t[j] = make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+  if (biased) {
+    const uint32_t bw[8] = {bb[0].x, bb[0].y, bb[0].z, bb[0].w, bb[1].x, bb[1].y, bb[1].z, bb[1].w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      t[j] = add2_rn(t[j], make_float2(__uint_as_float(bw[j] << 16), __uint_as_float(bw[j] & 0xFFFF0000u)));
+  }
   if constexpr (EPI != SVDQ_EPILOGUE_NONE) {
     if (act <= 0) {                                // the usual case, the same for all lanes
 #pragma unroll
@@ -438,7 +442,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           if (c + 8 < live) bb[1] = __ldg(reinterpret_cast<const uint4 *>(bias + c + 8));   // N % 8 == 0
         }
         dev::tmem_wait_ld();
-        finish16<EPI>(v, bb, p.gelu_col_begin - col0 - c, out);
+        finish16<EPI>(v, bias != nullptr, bb, p.gelu_col_begin - col0 - c, out);
         // row `lane`, 16-byte chunk k of the 32 columns at chunk k ^ (row / 2 % 4): few bank conflicts either way
         const int k = (c & 16) >> 3, x = (lane >> 1) & 3;
         *reinterpret_cast<uint4 *>(stage + lane * 64 + ((k ^ x) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
