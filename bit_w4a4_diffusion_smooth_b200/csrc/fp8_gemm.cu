@@ -32,6 +32,17 @@ bool few_is_faster(const Params &p, int sm_count) {
   return 57 * p.KS * few_rounds < 73 * p.KS * pair_rounds + 800;
 }
 
+// Whether an element of X [M][ldx], K columns, is one of Y [M][ldy], N columns.  Interleaved rows (one stride, columns
+// apart) are not; with two strides, what lies inside the other's range counts as shared.
+bool overlap(const void *X, int K, int ldx, const void *Y, int N, int ldy, int M) {
+  const int64_t x = static_cast<int64_t>(reinterpret_cast<uintptr_t>(X)) / 2;
+  const int64_t y = static_cast<int64_t>(reinterpret_cast<uintptr_t>(Y)) / 2;
+  if (y >= x + static_cast<int64_t>(M - 1) * ldx + K || x >= y + static_cast<int64_t>(M - 1) * ldy + N) return false;
+  if (M == 1 || ldx != ldy) return true;
+  const int64_t at = ((y - x) % ldx + ldx) % ldx;            // Y's first column in X's rows
+  return at < K || at + N > ldx;
+}
+
 int run(const char *fn, const void *X, int M, int K, int ldx, const int *offsets, int experts, const void *packed,
         const void *bias, int N, int epilogue, int gelu_col_begin, void *Y, int ldy, void *workspace,
         cudaStream_t stream) {
@@ -54,6 +65,7 @@ int run(const char *fn, const void *X, int M, int K, int ldx, const int *offsets
     return fail(SVDQ_ERR_ALIGNMENT, name + ": pointers must be 16-byte aligned");
   if (offsets && (reinterpret_cast<uintptr_t>(offsets) & 3u))
     return fail(SVDQ_ERR_ALIGNMENT, name + ": offsets must be 4-byte aligned");
+  if (overlap(X, K, ldx, Y, N, ldy, M)) return fail(SVDQ_ERR_INVALID_ARG, name + ": Y overlaps X");
   DeviceState *st = current_device_state();
   if (!st) return SVDQ_ERR_NOT_INITIALIZED;
 

@@ -6,8 +6,8 @@
 //
 // Up to 16 rows a tile (FUSED) each CTA quantizes the rows it needs itself,
 // stage by stage: X is small and sits in L2, and a quantizer kernel in front
-// would cost a launch and its latency, more than these calls take (2 rows,
-// 2560 -> 15360: 9.5 us against 10.9).  With more rows the CTAs' repeated
+// would cost a launch and its latency (2 rows, 2560 -> 15360: 8.9 us, and 10.9
+// with the quantizer in front).  With more rows the CTAs' repeated
 // quantizing takes longer than the weights (77 rows, 4096 -> 2560: 22 us
 // against 14), and the quantizer runs once in front.
 //
@@ -338,8 +338,8 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1)
           const int row = c.u.row0 + 4 * st + sub, k = (2 * c.kp + blk) * kBlock + chunk * 16;
           const uint4 *src = reinterpret_cast<const uint4 *>(p.X + static_cast<size_t>(row) * p.ldx + k);
           const bool live = row < c.u.end;
-          const uint4 v0 = live && k < p.K ? __ldg(src) : make_uint4(0, 0, 0, 0);
-          const uint4 v1 = live && k + 8 < p.K ? __ldg(src + 1) : make_uint4(0, 0, 0, 0);
+          const uint4 v0 = live && k < p.K ? __ldcg(src) : make_uint4(0, 0, 0, 0);
+          const uint4 v1 = live && k + 8 < p.K ? __ldcg(src + 1) : make_uint4(0, 0, 0, 0);
           raw[st][0] = v0.x, raw[st][1] = v0.y, raw[st][2] = v0.z, raw[st][3] = v0.w;
           raw[st][4] = v1.x, raw[st][5] = v1.y, raw[st][6] = v1.z, raw[st][7] = v1.w;
         }
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1)
     dev::tmem_wait_ld();
   };
   if constexpr (!S::FUSED)
-    if (warp >= 4) dev::grid_dependency_wait();           // nothing is written before it
+    if (warp >= 4 || split > 1) dev::grid_dependency_wait();   // nothing is written before it
   if (split == 1) {
     if (warp >= 4 && warp < 8) {
       int n = 0;
@@ -540,7 +540,7 @@ int launch(const char *fn, const Params &p, long long units, int sm_count, cudaS
   using S = Shape<TOK>;
   int rc = smem_optin_once<fp8_gemm_few_kernel<TOK, EPI>>(S::BYTES, fn);
   if (rc != SVDQ_OK) return rc;
-  // Split K where that still gives every CTA an SM of its own and four stages.
+  // Split K where that still gives every CTA an SM of its own and four blocks of 128 along K.
   int split = 1;
   while (split < 8 && units * split * 2 <= sm_count && p.KS >= 8 * split) split *= 2;
   const int grid = split > 1 ? static_cast<int>(units) * split : static_cast<int>(units < sm_count ? units : sm_count);

@@ -39,8 +39,8 @@ __global__ void __launch_bounds__(QUANT_THREADS)
     const int k0 = kw * 512 + lane * 16;
     const uint16_t *src = X + static_cast<size_t>(row) * ldx + k0;
     uint4 v[2];
-    v[0] = k0 < K ? __ldg(reinterpret_cast<const uint4 *>(src)) : make_uint4(0, 0, 0, 0);
-    v[1] = k0 + 8 < K ? __ldg(reinterpret_cast<const uint4 *>(src + 8)) : make_uint4(0, 0, 0, 0);
+    v[0] = k0 < K ? __ldcg(reinterpret_cast<const uint4 *>(src)) : make_uint4(0, 0, 0, 0);
+    v[1] = k0 + 8 < K ? __ldcg(reinterpret_cast<const uint4 *>(src + 8)) : make_uint4(0, 0, 0, 0);
     const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
     uint32_t out[4];
     const uint32_t byte = quantize16(w, out);

@@ -25,7 +25,9 @@
 // issue (4608 rows x 40 heads x 128: 30 us).
 #include <cuda_runtime.h>
 
+#include <cstdlib>
 #include <string>
+#include <utility>
 
 #include "device_common.cuh"
 #include "svdq_internal.h"
@@ -148,8 +150,8 @@ __global__ void __launch_bounds__(THREADS) rope_nd_kernel(const __grid_constant_
   for (int i = threadIdx.x; i < min(tokens, p.M - m0) * half_d; i += THREADS) {
     const int tk = i / half_d, pair = i % half_d;
     const long long at = static_cast<long long>(m0 + tk) * p.pos_row + p.axis[pair];
-    const double pos = p.pos_float ? static_cast<double>(__ldg(static_cast<const float *>(p.pos) + at))
-                                   : static_cast<double>(__ldg(static_cast<const int *>(p.pos) + at));
+    const double pos = p.pos_float ? static_cast<double>(__ldcg(static_cast<const float *>(p.pos) + at))
+                                   : static_cast<double>(__ldcg(static_cast<const int *>(p.pos) + at));
     double s, cs;
     sincos(pos * p.freq[pair], &s, &cs);
     turn[i] = make_float2(static_cast<float>(cs), static_cast<float>(p.inverse ? -s : s));
@@ -243,6 +245,31 @@ bool apart(int64_t row, int64_t head, int M, int heads, int D) {
   if (heads == 1) return row >= D;
   return row <= head ? row >= D && head / M >= row : head >= D && row / heads >= head;
 }
+// Whether a vector of `b` (Y's, `heads_b` of them in a row) shares an element with one of `a`, where both have the
+// same strides; what two tensors of different strides share is not looked for.
+bool overlap(const void *a, int64_t a_row, int64_t a_head, int heads_a, const void *b, int64_t b_row, int64_t b_head,
+             int heads_b, int M, int D) {
+  if ((M > 1 && a_row != b_row) || (heads_a > 1 && heads_b > 1 && a_head != b_head)) return a == b;
+  const int64_t delta = (static_cast<const uint8_t *>(b) - static_cast<const uint8_t *>(a)) / 2;
+  const int64_t head = heads_a > 1 ? a_head : b_head;
+  // m b_row + h head + d = delta, with |d| < D, m and h a difference of two rows and of two heads: the wider stride's
+  // factor is one of the two next to the quotient, then the other's
+  struct Dim {
+    int64_t step, lo, hi;
+  } wide = {M > 1 ? b_row : 0, 1 - M, M - 1}, near = {heads_a > 1 || heads_b > 1 ? head : 0, 1 - heads_b, heads_a - 1};
+  if (wide.step < near.step) std::swap(wide, near);
+  const auto quotient = [](int64_t n, const Dim &dim) {
+    return dim.step > 0 ? n / dim.step - (n % dim.step < 0) : 0;
+  };
+  const int64_t i0 = quotient(delta, wide);
+  for (int64_t i = i0; i <= i0 + 1; ++i) {
+    if (i < wide.lo || i > wide.hi) continue;
+    const int64_t rest = delta - i * wide.step, j0 = quotient(rest, near);
+    for (int64_t j = j0; j <= j0 + 1; ++j)
+      if (j >= near.lo && j <= near.hi && std::abs(rest - j * near.step) < D) return true;
+  }
+  return false;
+}
 int check_tensor(const char *which, const rope_nd_tensor_t &t, int M, int D) {
   const std::string name = std::string("rope_nd: ") + which;
   if (!t.X || !t.Y) return fail(SVDQ_ERR_INVALID_ARG, name + ": null pointer");
@@ -288,6 +315,13 @@ extern "C" int rope_nd(const rope_nd_tensor_t *Q, const rope_nd_tensor_t *K, int
   if (inverse && (Q->norm || (K && K->norm)))
     return fail(SVDQ_ERR_INVALID_ARG, "rope_nd: the inverse undoes the turn only and takes no norm");
   if (reinterpret_cast<uintptr_t>(pos) & 3u) return fail(SVDQ_ERR_ALIGNMENT, "rope_nd: pos must be 4-byte aligned");
+  const auto shared = [&](const rope_nd_tensor_t &a, bool out, const rope_nd_tensor_t &b) {   // a's X or Y and b's Y
+    return out ? overlap(a.Y, a.y_row, a.y_head, a.heads, b.Y, b.y_row, b.y_head, b.heads, M, D)
+               : overlap(a.X, a.x_row, a.x_head, a.heads, b.Y, b.y_row, b.y_head, b.heads, M, D);
+  };
+  if ((Q->X != Q->Y && shared(*Q, false, *Q)) ||
+      (K && ((K->X != K->Y && shared(*K, false, *K)) || shared(*Q, false, *K) || shared(*K, false, *Q) || shared(*Q, true, *K))))
+    return fail(SVDQ_ERR_INVALID_ARG, "rope_nd: a Y overlaps another Y, another tensor's X, or part of its own");
   DeviceState *st = current_device_state();
   if (!st) return SVDQ_ERR_NOT_INITIALIZED;
   for (int i = 0; i < 2; ++i) {

@@ -351,6 +351,12 @@ def _on(device, stream, call, *args):
         return call(*args, stream.cuda_stream)
 
 
+def _aligned(t):
+    """A vector as the kernels take it: contiguous, on a 16-byte boundary (`t` itself if it is)."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class FP8Linear:
     """Y = epilogue(q(X) q(W) + b) in block-scaled FP8: e4m3 codes under one power-of-two scale per 128 elements
     along K, for every row of X and every column of W (for projections that 4 bits lose too much of).
@@ -378,8 +384,8 @@ class FP8Linear:
                                  or bias.device != self.device):
             raise ValueError(f"{name}: bias must be bf16 {[*lead, self.N]} on {self.device}")
         _init_on(self.device)
-        self.bias = bias.contiguous() if bias is not None else None
         with torch.cuda.device(self.device):
+            self.bias = None if bias is None else _aligned(bias)
             self.packed = lib.fp8_pack_weights(weight if weight.stride(-1) == 1 else weight.contiguous())
             torch.cuda.current_stream().synchronize()   # ready on every stream from here on
 
@@ -471,8 +477,10 @@ class RotaryND:
             if w is not None and (w.dtype != torch.bfloat16 or w.numel() != D or w.device != self.device):
                 raise ValueError(f"RotaryND: a norm weight must be bf16 [{D}] on {self.device}")
         _init_on(self.device)
-        self.q_norm = None if q_norm is None else q_norm.contiguous()
-        self.k_norm = None if k_norm is None else k_norm.contiguous()
+        with torch.cuda.device(self.device):
+            self.q_norm = None if q_norm is None else _aligned(q_norm)
+            self.k_norm = None if k_norm is None else _aligned(k_norm)
+            torch.cuda.current_stream().synchronize()   # ready on every stream from here on
         pairs = [(a, float(theta) ** (-2.0 * j / d)) for a, d in enumerate(axis_dims) for j in range(d // 2)]
         self.plan = lib.RopePlan(D, self.axes, lib.ROPE_ND_INTERLEAVED if interleaved else lib.ROPE_ND_HALF)
         for i, (a, f) in enumerate(pairs):
@@ -480,22 +488,19 @@ class RotaryND:
 
     def __call__(self, q, k, pos, q_out=None, k_out=None, inverse=False, stream=None):
         """q: bf16 CUDA [M, heads, D] (any row and head strides), k likewise or None; pos: int32 or float32
-        [M, axes].  Returns (q_out, k_out); q_out may be q, k_out may be k.  inverse: turns back."""
+        [M, axes].  Returns (q_out, k_out); q_out may be q, k_out may be k.  inverse: turns back (not with norm
+        weights)."""
         return _on(self.device, stream, self._call, q, k, pos, q_out, k_out, inverse)
 
     def _call(self, q, k, pos, q_out, k_out, inverse, s):
         if k is None and k_out is not None:
             raise ValueError("RotaryND: k_out without k")
-        if q.dim() != 3 or pos.dim() != 2 or (k is not None and k.dim() != 3):
-            raise ValueError(f"RotaryND: q and k must be [M, heads, {self.D}] and pos [M, {self.axes}]")
+        if pos.get_device() != self.device.index:
+            raise ValueError(f"RotaryND: every tensor must be on {self.device}, got pos on {pos.device}")
         if q_out is None:
             q_out = torch.empty_like(q)
         if k_out is None and k is not None:
             k_out = torch.empty_like(k)
-        index = self.device.index
-        for t in (q, pos, q_out) if k is None else (q, k, pos, q_out, k_out):
-            if t.get_device() != index:
-                raise ValueError(f"RotaryND: every tensor must be on {self.device}, got {t.device}")
         lib.rope_nd(q, k, self.plan, pos, q_out, k_out, self.q_norm, None if k is None else self.k_norm, inverse,
                     self.eps, s)
         return q_out, k_out

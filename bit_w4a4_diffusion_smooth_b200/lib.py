@@ -780,15 +780,16 @@ def fp8_linear_grouped(X, offsets, packed, bias, N, epilogue, gelu_col_begin, Y,
         _fp8_workspace(workspace, M, K, E), _stream(stream)))
 
 
-def _rope_tensor(x, y, norm, M, D, dtype, name):
-    """Checks one tensor's heads [M, heads, D] and returns its packed rope_nd_tensor."""
+def _rope_tensor(x, y, norm, M, D, dtype, device, name):
+    """Checks one tensor's heads [M, heads, D] and returns its packed rope_nd_tensor.  `device`: a CUDA device's
+    index (a host tensor's is -1)."""
     shape = x.shape
     if len(shape) != 3 or shape[0] != M or shape[2] != D or y.shape != shape:
         raise ValueError(f"{name} must be [{M}, heads, {D}] and its output alike, got {tuple(x.shape)} and "
                          f"{tuple(y.shape)}")
-    if x.dtype is not dtype or y.dtype is not dtype or not (x.is_cuda and y.is_cuda):
-        raise ValueError(f"{name} and its output must be {dtype} CUDA tensors, got {x.dtype} on {x.device} and "
-                         f"{y.dtype} on {y.device}")
+    if x.dtype is not dtype or y.dtype is not dtype or x.get_device() != device or y.get_device() != device:
+        raise ValueError(f"{name} and its output must be {dtype} on cuda:{device}, where pos is, got {x.dtype} on "
+                         f"{x.device} and {y.dtype} on {y.device}")
     H = shape[1]
     (xr, xh, xd), (yr, yh, yd) = x.stride(), y.stride()
     if xd != 1 or yd != 1:
@@ -799,23 +800,24 @@ def _rope_tensor(x, y, norm, M, D, dtype, name):
         xh = yh = 0
     if norm is None:
         return ROPE_TENSOR.pack(x.data_ptr(), xr, xh, y.data_ptr(), yr, yh, 0, H)
-    if norm.dtype is not dtype or norm.numel() != D or not norm.is_contiguous() or not norm.is_cuda:
-        raise ValueError(f"a norm weight must be {dtype} CUDA [{D}]")
+    if norm.dtype is not dtype or norm.numel() != D or not norm.is_contiguous() or norm.get_device() != device:
+        raise ValueError(f"a norm weight must be {dtype} [{D}] on cuda:{device}")
     return ROPE_TENSOR.pack(x.data_ptr(), xr, xh, y.data_ptr(), yr, yh, norm.data_ptr(), H)
 
 
 def rope_nd(q, k, plan, pos, q_out, k_out, q_norm=None, k_norm=None, inverse=False, eps=1e-6, stream=None):
     """Enqueues the rotary positions of q [M, heads, D] and k (likewise, or None), bf16 CUDA, into q_out and
-    k_out (which may be q and k).  pos: int32 or float32 CUDA [M, axes]; norms: bf16 CUDA [D] or None."""
+    k_out (which may be q and k).  pos: int32 or float32 CUDA [M, axes]; norms: bf16 CUDA [D] or None.  stream: a
+    torch stream or a raw handle, else the current one."""
     import torch
-    shape, kind = pos.shape, pos.dtype
+    shape, kind, device = pos.shape, pos.dtype, pos.get_device()
     if len(shape) != 2 or shape[1] != plan.axes or (plan.axes > 1 and pos.stride(1) != 1):
         raise ValueError(f"pos must be [M, {plan.axes}] with unit stride in its last dimension, got {tuple(shape)}")
-    if (kind is not torch.int32 and kind is not torch.float32) or not pos.is_cuda:
+    if (kind is not torch.int32 and kind is not torch.float32) or device < 0:
         raise ValueError(f"pos must be an int32 or float32 CUDA tensor, got {kind} on {pos.device}")
     M = _c_int(shape[0], "the number of rows")
-    tq = _rope_tensor(q, q_out, q_norm, M, plan.D, torch.bfloat16, "q")
-    tk = None if k is None else _rope_tensor(k, k_out, k_norm, M, plan.D, torch.bfloat16, "k")
+    tq = _rope_tensor(q, q_out, q_norm, M, plan.D, torch.bfloat16, device, "q")
+    tk = None if k is None else _rope_tensor(k, k_out, k_norm, M, plan.D, torch.bfloat16, device, "k")
     rc = load().rope_nd(tq, tk, M, plan, pos.data_ptr(), pos.stride(0) if M > 1 else 0, kind is torch.float32,
                         inverse, eps, stream if type(stream) is int else _stream(stream))
     if rc != OK:

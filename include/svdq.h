@@ -557,7 +557,8 @@ int svdq_linear_int4(const uint8_t *a_codes, const void *a_scales, const void *U
 int fp8_weight_size(int K, int N, int experts, size_t *bytes);
 
 /* Bytes of the workspace of a call: the quantized activations, or 0 where the
- * call quantizes them on the way in (16 rows, or 8 an expert on average).  Rules: M >= 1, K >= 8, K % 8 == 0, 1 <= experts <= FP8_MAX_EXPERTS. */
+ * call quantizes them on the way in (16 rows, or 8 an expert on average).
+ * Rules: M >= 1, K >= 8, K % 8 == 0, 1 <= experts <= FP8_MAX_EXPERTS. */
 int fp8_workspace_size(int M, int K, int experts, size_t *bytes);
 
 /*
@@ -578,7 +579,9 @@ int fp8_pack_weights(const void *W, int K, int N, int ldw, int64_t expert_stride
  * use until the call has run on the stream (calls that may overlap take
  * workspaces of their own).
  * Rules: 1 <= M <= FP8_MAX_ROWS, K >= 8, K % 8 == 0, ldx >= K, ldx % 8 == 0,
- * N >= 8, N % 8 == 0, ldy >= N, ldy % 8 == 0, 0 <= gelu_col_begin <= N.
+ * N >= 8, N % 8 == 0, ldy >= N, ldy % 8 == 0, 0 <= gelu_col_begin <= N; no
+ * element of Y is one of X (rows of one stride may interleave, other ranges
+ * must lie apart).
  */
 int fp8_linear(const void *X, int M, int K, int ldx, const void *packed, const void *bias, int N, int epilogue,
                int gelu_col_begin, void *Y, int ldy, void *workspace, svdq_stream_t stream);
@@ -636,7 +639,8 @@ typedef struct rope_nd_tensor {
  * Rules: 1 <= M <= ROPE_ND_MAX_ROWS; 8 <= D <= 256, D % 8 == 0; 1 <= axes <= D/2; axis[i] < axes;
  * 1 <= heads <= 65535; strides multiples of 8; pointers 16-byte aligned (pos
  * 4-byte); pos_row >= 0 (0: one position for all rows); the heads of a Y must
- * not overlap one another.
+ * not overlap one another, the other Y, the other tensor's X, or its own X
+ * unless it is that X (checked where the strides are the same).
  */
 int rope_nd(const rope_nd_tensor_t *Q, const rope_nd_tensor_t *K, int M, const rope_nd_plan_t *plan, const void *pos,
             int64_t pos_row, int pos_is_float, int inverse, float eps, svdq_stream_t stream);

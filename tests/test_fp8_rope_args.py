@@ -93,6 +93,58 @@ def test_rope_refuses(kw, want):
     assert _rope(**kw) == want
 
 
+@pytest.mark.parametrize("kw", [
+    # bytes: rows of 64, 4 rows from 256 on: 256 .. 512; Y of the same rows, one element run in them
+    dict(x=256, y=256), dict(x=256, y=256 + 48), dict(x=256, y=496), dict(x=496, y=256), dict(x=256, y=272, ldx=32, ldy=40),
+    dict(x=256, y=256 + 32, ldx=40, ldy=40), dict(M=1, x=256, y=304), dict(x=256, y=256 + 64 + 16, ldx=64, ldy=64)])
+def test_fp8_refuses_a_y_on_top_of_x(kw):
+    kw = dict(dict(M=4, ldx=32, ldy=32), **kw)
+    x, y = ctypes.c_void_p(kw.pop("x")), ctypes.c_void_p(kw.pop("y"))
+    assert _linear(x=x, y=y, K=32, N=32, **kw) == lib.ERR_INVALID_ARG
+    assert b"overlaps" in lib.load().svdq_last_error_string()
+
+
+@pytest.mark.parametrize("kw", [
+    # apart, or interleaved rows: past the check, refused only for want of a device
+    dict(x=256, y=512), dict(x=512, y=256), dict(x=256, y=256 + 64, ldx=64, ldy=64), dict(x=320, y=256, ldx=64, ldy=64),
+    dict(x=256, y=256 + 96, ldx=80, ldy=80), dict(M=1, x=256, y=320)])
+def test_fp8_takes_a_y_beside_x(kw):
+    kw = dict(dict(M=4, ldx=32, ldy=32), **kw)
+    x, y = ctypes.c_void_p(kw.pop("x")), ctypes.c_void_p(kw.pop("y"))
+    if torch.cuda.is_available():
+        pytest.skip("the call would run")
+    assert _linear(x=x, y=y, K=32, N=32, **kw) == lib.ERR_NOT_INITIALIZED
+
+
+def _cells(X, row, head, heads, M, D=16):
+    return {X // 2 + m * row + h * head + d for m in range(M) for h in range(heads) for d in range(D)}
+
+
+def test_rope_refuses_shared_elements_and_only_those():
+    """Every pair of layouts of one buffer against a count of the elements they share."""
+    if torch.cuda.is_available():
+        pytest.skip("the accepted calls would run")
+    D, seen = 16, [0, 0]
+    layouts = [(M, row, head, hq, hk) for M, row, head, hq, hk in (
+        (3, 96, 16, 2, 2), (3, 96, 16, 4, 1), (2, 96, 32, 2, 1), (4, 16, 80, 2, 2), (1, 16, 48, 2, 1), (3, 48, 16, 1, 2))]
+    for M, row, head, hq, hk in layouts:
+        for a in range(0, 320, 8):
+            for b in (0, 16, 40, 64, 128, 400):
+                base = 4096
+                qx, kx, qy, ky = base, base + 2 * a, base + 2 * 2000, base + 2 * (2000 + b)
+                for q, k in (((qx, qy), (kx, ky)), ((qx, qx), (kx, kx)), ((qx, kx), (kx, qx)), ((qx, kx), (ky, ky)),
+                             ((qx, qx), (kx, ky))):
+                    c = [_cells(v, row, head, n, M) for v, n in ((q[0], hq), (q[1], hq), (k[0], hk), (k[1], hk))]
+                    bad = (q[0] != q[1] and c[0] & c[1]) or (k[0] != k[1] and c[2] & c[3]) or c[0] & c[3] or \
+                        c[2] & c[1] or c[1] & c[3]
+                    rc = _rope(q=(q[0], row, head, q[1], row, head, None, hq),
+                               k=(k[0], row, head, k[1], row, head, None, hk), M=M)
+                    assert rc == (lib.ERR_INVALID_ARG if bad else lib.ERR_NOT_INITIALIZED), (M, row, head, hq, hk, q, k)
+                    seen[not bad] += 1
+    assert min(seen) > 500, seen
+    assert _rope(q=(16, 32, 16, 4096, 32, 16, None, 2), k=(4096, 64, 16, 9999 * 16, 64, 16, None, 2)) == lib.ERR_INVALID_ARG
+
+
 def test_rope_refuses_an_axis_that_pos_lacks():
     p = _plan()
     p.axis[3] = 2

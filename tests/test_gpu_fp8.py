@@ -284,6 +284,24 @@ def test_layers_refuse():
             call()
 
 
+def test_misaligned_bias_and_rows_that_interleave():
+    K, N = 136, 264
+    W, b = (bf16(rand(seed, *shape)).to(G.DEV) for seed, shape in ((1, (K, N)), (2, (N,))))
+    off = torch.zeros(N + 3, dtype=torch.bfloat16, device=G.DEV)
+    off[3:] = b
+    fc, want = layer.FP8Linear(W, off[3:]), layer.FP8Linear(W, b)
+    for M in (5, 77, 300):
+        X = bf16(rand(M, M, K)).to(G.DEV)
+        both = G.poisoned_bf16(M, K + N + 8)
+        both[:, :K] = X
+        fc(both[:, :K], Y=both[:, K:K + N])
+        assert torch.equal(both[:, K:K + N], want(X)) and torch.equal(both[:, :K], X)
+        assert torch.isnan(both[:, K + N:]).all()
+        with pytest.raises(lib.SvdqError):
+            fc(both[:, :K], Y=both[:, 8:8 + N])
+    G.check_ok()
+
+
 def test_two_streams_and_two_graphs_share_a_layer():
     """Calls of one instance that overlap on two streams, and two captured graphs replayed at once, have
     workspaces of their own."""

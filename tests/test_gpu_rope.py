@@ -166,6 +166,21 @@ def test_refusals():
             call()
 
 
+def test_outputs_on_top_of_other_inputs_and_misaligned_norms():
+    turn = layer.RotaryND([32, 32])
+    q, k, pos = rand(1, 6, 2, 64), rand(2, 6, 2, 64), torch.zeros(6, 2, dtype=torch.int32, device=G.DEV)
+    for kw in (dict(q_out=k, k_out=q), dict(q_out=k), dict(k_out=q), dict(q_out=q, k_out=q)):
+        with pytest.raises(lib.SvdqError):
+            turn(q, k, pos, **kw)
+    w = rand(3, 64)
+    off = torch.zeros(67, dtype=torch.bfloat16, device=G.DEV)
+    off[3:] = w
+    a, b = layer.RotaryND([32, 32], q_norm=off[3:], k_norm=off[3:]), layer.RotaryND([32, 32], q_norm=w, k_norm=w)
+    for x, y in zip(a(q, k, pos), b(q, k, pos)):
+        assert torch.equal(x, y)
+    G.check_ok()
+
+
 def test_streams_and_graphs():
     turn = layer.RotaryND([44, 42, 42])
     x = rand(1, 800, 4, 128)
