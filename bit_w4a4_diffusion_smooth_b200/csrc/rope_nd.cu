@@ -9,20 +9,25 @@
 //
 // Angles are taken in float64: a float32 product pos * f is off by up to
 // pos 2^-24 radians, which at positions in the ten thousands is already bf16's
-// own step.  They cost little: a block computes each of its tokens' D/2 angles
-// once, into shared memory, and every head of those tokens uses them, so the
-// call needs no table in memory and no launch to fill one.  Everything else is
-// float32, rounded once to bf16.
+// own step.  They are counted in turns, so that the whole turns come off with
+// one rounding; what is left, within half a turn, goes to float32 (off by at
+// most 2^-26 turns), and its cosine and sine are float32 like everything else,
+// rounded once to bf16.  (Float64 cosines and sines gave no other bits that
+// count and took 0.3 us more, 4608 rows.)  A block computes each of its tokens'
+// D/2 angles once, into shared memory, and every head of those tokens uses
+// them, so the call needs no table in memory and no launch to fill one.
 //
 // Bound by memory: each element is read and written once (4 bytes).  A lane
 // holds 4 pairs of a head (8 elements): 16 contiguous bytes in the interleaved
 // pairing (2i, 2i + 1), two runs of 8 bytes in the half-split one (i, i + D/2).
 // A group of lanes keeps one token's cos and sin, times the norm weights of one
 // tensor, in registers and walks over that tensor's heads, four heads' loads in
-// flight at a time; the first four are under way while the block computes its
-// angles.  The arithmetic runs on f32x2 instructions, two pairs at once: with
+// flight at a time, each place loaded again as soon as its head is turned; the
+// first four are under way while the block computes its angles.  64 registers
+// let 8 blocks share an SM (7: 20.6 us, 9, with spills: 22.8, 8: 19.4, for 4608
+// normed rows x 40 heads x 128).  The arithmetic runs on f32x2 instructions, two pairs at once: with
 // scalar ones, and the tensor chosen head by head, the normed call was bound by
-// issue (4608 rows x 40 heads x 128: 30 us).
+// issue (30 us for those rows).
 #include <cuda_runtime.h>
 
 #include <cstdlib>
@@ -36,7 +41,8 @@ namespace svdq {
 namespace rope {
 namespace {
 
-constexpr int THREADS = 128;      // (256: 22.2 us where 128 take 20.5, 4608 normed rows x 40 heads x 128)
+constexpr int THREADS = 128;
+constexpr int BLOCKS = 8;         // on an SM
 constexpr int MAX_D = 256;
 
 struct Tensor {
@@ -55,7 +61,7 @@ struct Params {
   int q_groups;                 // of which the first so many take the query's heads
   int pos_float, inverse;
   float eps, inv_d;
-  double freq[MAX_D / 2];
+  double freq[MAX_D / 2];       // turns per position
   unsigned char axis[MAX_D / 2];
 };
 
@@ -109,7 +115,7 @@ __device__ __forceinline__ void split(const uint32_t (&w)[4], float2 (&x0)[2], f
 }
 
 template <bool HALF, bool NORM>
-__global__ void __launch_bounds__(THREADS) rope_nd_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(THREADS, BLOCKS) rope_nd_kernel(const __grid_constant__ Params p) {
   extern __shared__ float2 turn[];            // [tokens][D/2] (cos, sin)
   dev::grid_dependency_wait();
   dev::grid_launch_dependents();
@@ -133,28 +139,31 @@ __global__ void __launch_bounds__(THREADS) rope_nd_kernel(const __grid_constant_
   uint16_t *y = t.y + m * t.y_row;
 
   uint32_t w[UNROLL][4];
-  const auto load = [&](int round) {
+  const auto load = [&](int i, int round) {
+    const int h = first + (round + i) * step;
+    if (h < heads) {
+      load8<HALF>(x + h * t.x_head, c, p.D, w[i]);
+    } else {
 #pragma unroll
-    for (int i = 0; i < UNROLL; ++i) {
-      const int h = first + (round + i) * step;
-      if (h < heads) {
-        load8<HALF>(x + h * t.x_head, c, p.D, w[i]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) w[i][k] = 0u;
-      }
+      for (int k = 0; k < 4; ++k) w[i][k] = 0u;
     }
   };
-  load(0);
+#pragma unroll
+  for (int i = 0; i < UNROLL; ++i) load(i, 0);
+  const bool normed = NORM && t.norm != nullptr;
+  uint32_t nw[4] = {0u, 0u, 0u, 0u};
+  if constexpr (NORM)
+    if (on && normed) load8<HALF>(t.norm, c, p.D, nw);
 
   for (int i = threadIdx.x; i < min(tokens, p.M - m0) * half_d; i += THREADS) {
     const int tk = i / half_d, pair = i % half_d;
     const long long at = static_cast<long long>(m0 + tk) * p.pos_row + p.axis[pair];
     const double pos = p.pos_float ? static_cast<double>(__ldcg(static_cast<const float *>(p.pos) + at))
                                    : static_cast<double>(__ldcg(static_cast<const int *>(p.pos) + at));
-    double s, cs;
-    sincos(pos * p.freq[pair], &s, &cs);
-    turn[i] = make_float2(static_cast<float>(cs), static_cast<float>(p.inverse ? -s : s));
+    const double turns = pos * p.freq[pair];
+    float s, cs;
+    sincospif(2.0f * static_cast<float>(turns - rint(turns)), &s, &cs);
+    turn[i] = make_float2(cs, p.inverse ? -s : s);
   }
   __syncthreads();
   // y0 = x0 c0 - x1 s1, y1 = x0 s0 + x1 c1: cos and sin, with the norm weight of the element they multiply
@@ -166,11 +175,8 @@ __global__ void __launch_bounds__(THREADS) rope_nd_kernel(const __grid_constant_
     c0[i] = c1[i] = make_float2(a.x, b.x);
     s0[i] = s1[i] = make_float2(a.y, b.y);
   }
-  const bool normed = NORM && t.norm != nullptr;
   if constexpr (NORM) {
     if (on && normed) {
-      uint32_t nw[4];
-      load8<HALF>(t.norm, c, p.D, nw);
       float2 g0[2], g1[2];
       split<HALF>(nw, g0, g1);
 #pragma unroll
@@ -186,7 +192,6 @@ __global__ void __launch_bounds__(THREADS) rope_nd_kernel(const __grid_constant_
   for (int i = 0; i < 2; ++i) s1[i] = make_float2(-s1[i].x, -s1[i].y);
 
   for (int round = 0; round < rounds; round += UNROLL) {
-    uint32_t out[UNROLL][4];
     float scale[UNROLL];
     if constexpr (NORM) {                     // four heads' sums side by side: their shuffles overlap
 #pragma unroll
@@ -207,7 +212,9 @@ __global__ void __launch_bounds__(THREADS) rope_nd_kernel(const __grid_constant_
     }
 #pragma unroll
     for (int i = 0; i < UNROLL; ++i) {
+      if (round + i >= rounds) break;
       float2 x0[2], x1[2], y0[2], y1[2];
+      uint32_t out[4];
       split<HALF>(w[i], x0, x1);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -221,20 +228,17 @@ __global__ void __launch_bounds__(THREADS) rope_nd_kernel(const __grid_constant_
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         if constexpr (HALF) {
-          out[i][k] = pack2(y0[k].x, y0[k].y);
-          out[i][2 + k] = pack2(y1[k].x, y1[k].y);
+          out[k] = pack2(y0[k].x, y0[k].y);
+          out[2 + k] = pack2(y1[k].x, y1[k].y);
         } else {
-          out[i][2 * k] = pack2(y0[k].x, y1[k].x);
-          out[i][2 * k + 1] = pack2(y0[k].y, y1[k].y);
+          out[2 * k] = pack2(y0[k].x, y1[k].x);
+          out[2 * k + 1] = pack2(y0[k].y, y1[k].y);
         }
       }
-    }
-    // the next heads' loads before these stores: no lane stores what another loads
-    if (round + UNROLL < rounds) load(round + UNROLL);
-#pragma unroll
-    for (int i = 0; i < UNROLL; ++i) {
+      // this place's next head before the store: no lane stores what another loads
+      if (round + UNROLL < rounds) load(i, round + UNROLL);
       const int h = first + (round + i) * step;
-      if (h < heads) store8<HALF>(y + h * t.y_head, c, p.D, out[i]);
+      if (h < heads) store8<HALF>(y + h * t.y_head, c, p.D, out);
     }
   }
 }
@@ -307,7 +311,7 @@ extern "C" int rope_nd(const rope_nd_tensor_t *Q, const rope_nd_tensor_t *K, int
   for (int i = 0; i < D / 2; ++i) {
     if (plan->axis[i] >= plan->axes) return fail(SVDQ_ERR_SHAPE, "rope_nd: a pair's axis is outside [0, axes)");
     p.axis[i] = plan->axis[i];
-    p.freq[i] = plan->freq[i];
+    p.freq[i] = plan->freq[i] / 6.283185307179586;   // radians to turns
   }
   int rc = check_tensor("query", *Q, M, D);
   if (rc == SVDQ_OK && K) rc = check_tensor("key", *K, M, D);
