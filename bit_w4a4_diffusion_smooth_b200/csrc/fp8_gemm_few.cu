@@ -38,6 +38,7 @@
 // the abort flag, and the CTA drains its copies and MMAs, frees TMEM and ends.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <string>
 
 #include "fp8_gemm.cuh"
@@ -535,28 +536,50 @@ __global__ void __launch_bounds__(Shape<TOK>::THREADS, 1)
   }
 }
 
+// How many clusters of 2^log2 CTAs the current device runs at a time.  A cluster needs its SMs in one GPC, so clusters of
+// 4 and 8 leave some SMs out (33 and 15 on a B200 with 148).  Asked once per device and size.
+template <auto Kernel>
+int resident_clusters(const cudaLaunchConfig_t &cfg, int log2) {
+  static std::atomic<int> known[64][4];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if ((n = known[dev][log2].load(std::memory_order_relaxed)) != 0) return n - 1;
+  if (cudaOccupancyMaxActiveClusters(&n, Kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  known[dev][log2].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
 template <int TOK, int EPI>
 int launch(const char *fn, const Params &p, long long units, int sm_count, cudaStream_t stream) {
   using S = Shape<TOK>;
   int rc = smem_optin_once<fp8_gemm_few_kernel<TOK, EPI>>(S::BYTES, fn);
   if (rc != SVDQ_OK) return rc;
-  // Split K where that still gives every CTA an SM of its own and four blocks of 128 along K.
-  int split = 1;
-  while (split < 8 && units * split * 2 <= sm_count && p.KS >= 8 * split) split *= 2;
-  const int grid = split > 1 ? static_cast<int>(units) * split : static_cast<int>(units < sm_count ? units : sm_count);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = split;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
+  attr[1].val.clusterDim.x = attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(S::THREADS);
   cfg.dynamicSmemBytes = S::BYTES;
   cfg.stream = stream;
   cfg.attrs = attr;
+  // Split K where that leaves every CTA four blocks of 128 along K and all clusters still run at once: a second wave
+  // of them costs more than a split saves (16 rows, 4096 -> 2048, 16 units: 14.2 us as clusters of 8, of which 15 fit;
+  // 7.6 us as clusters of 4).
+  int split = 1;
+  for (int log2 = 1; log2 <= 3 && p.KS >= 4 << log2 && units << log2 <= sm_count; ++log2) {
+    attr[1].val.clusterDim.x = 1 << log2;
+    cfg.gridDim = dim3(1 << log2);
+    cfg.numAttrs = 2;
+    if (units > resident_clusters<fp8_gemm_few_kernel<TOK, EPI>>(cfg, log2)) break;
+    split = 1 << log2;
+  }
+  attr[1].val.clusterDim.x = split;
+  cfg.gridDim = dim3(split > 1 ? static_cast<int>(units) * split : static_cast<int>(units < sm_count ? units : sm_count));
   cfg.numAttrs = split > 1 ? 2 : 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, fp8_gemm_few_kernel<TOK, EPI>, p, split);
   if (e == cudaSuccess) e = cudaGetLastError();
