@@ -13,7 +13,7 @@
 // one rounding; what is left, within half a turn, goes to float32 (off by at
 // most 2^-26 turns), and its cosine and sine are float32 like everything else,
 // rounded once to bf16.  (Float64 cosines and sines gave no other bits that
-// count and took 0.3 us more, 4608 rows.)  A block computes each of its tokens'
+// count and took 0.3 us more for 4608 rows.)  A block computes each of its tokens'
 // D/2 angles once, into shared memory, and every head of those tokens uses
 // them, so the call needs no table in memory and no launch to fill one.
 //
@@ -24,8 +24,8 @@
 // tensor, in registers and walks over that tensor's heads, four heads' loads in
 // flight at a time, each place loaded again as soon as its head is turned; the
 // first four are under way while the block computes its angles.  64 registers
-// let 8 blocks share an SM (7: 20.6 us, 9, with spills: 22.8, 8: 19.4, for 4608
-// normed rows x 40 heads x 128).  The arithmetic runs on f32x2 instructions, two pairs at once: with
+// let 8 blocks share an SM (4608 normed rows x 40 heads x 128: 18.6 us; 20.2
+// with 7, 22.8 with 9, which spill).  The arithmetic runs on f32x2 instructions, two pairs at once: with
 // scalar ones, and the tensor chosen head by head, the normed call was bound by
 // issue (30 us for those rows).
 #include <cuda_runtime.h>
@@ -44,6 +44,7 @@ namespace {
 constexpr int THREADS = 128;
 constexpr int BLOCKS = 8;         // on an SM
 constexpr int MAX_D = 256;
+static_assert(4 * (MAX_D / 8) <= THREADS, "a token's heads go to four groups of lanes at least");
 
 struct Tensor {
   const uint16_t *x;
@@ -116,12 +117,24 @@ __device__ __forceinline__ void split(const uint32_t (&w)[4], float2 (&x0)[2], f
 
 template <bool HALF, bool NORM>
 __global__ void __launch_bounds__(THREADS, BLOCKS) rope_nd_kernel(const __grid_constant__ Params p) {
-  extern __shared__ float2 turn[];            // [tokens][D/2] (cos, sin)
-  dev::grid_dependency_wait();
-  dev::grid_launch_dependents();
+  __shared__ float2 turn[THREADS];            // [tokens][D/2] (cos, sin)
   const int half_d = p.D / 2, lanes = 1 << p.lanes_log2;
   const int tokens = THREADS >> (p.lanes_log2 + p.groups_log2);
   const int m0 = static_cast<int>(blockIdx.x) * tokens;
+  // A thread has at most one angle: with four groups a token or more, tokens D / 2 <= THREADS.  Its pair's axis and
+  // frequency are loaded through generic addresses: as constants, which the compiler would read them as, a warp's 32
+  // pairs took 32 accesses one after the other (9000 rows x 4 heads x 64: 7.8 us against 4.5).
+  const int a_tok = static_cast<int>(threadIdx.x) / half_d, pair = static_cast<int>(threadIdx.x) % half_d;
+  const double *freq = p.freq;
+  const unsigned char *axis = p.axis;
+  asm volatile("" : "+l"(freq), "+l"(axis));
+  const double pair_freq = freq[pair];
+  const int pair_axis = axis[pair];
+  dev::grid_dependency_wait();
+  dev::grid_launch_dependents();
+  int raw = 0;
+  if (a_tok < tokens && m0 + a_tok < p.M)
+    raw = __ldcg(static_cast<const int *>(p.pos) + (m0 + a_tok) * p.pos_row + pair_axis);
   const int c = threadIdx.x & (lanes - 1);                              // 8 elements of a head; past D / 8 idle
   const int group = (threadIdx.x >> p.lanes_log2) & ((1 << p.groups_log2) - 1);
   const int tok = threadIdx.x >> (p.lanes_log2 + p.groups_log2);
@@ -155,16 +168,10 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rope_nd_kernel(const __grid_c
   if constexpr (NORM)
     if (on && normed) load8<HALF>(t.norm, c, p.D, nw);
 
-  for (int i = threadIdx.x; i < min(tokens, p.M - m0) * half_d; i += THREADS) {
-    const int tk = i / half_d, pair = i % half_d;
-    const long long at = static_cast<long long>(m0 + tk) * p.pos_row + p.axis[pair];
-    const double pos = p.pos_float ? static_cast<double>(__ldcg(static_cast<const float *>(p.pos) + at))
-                                   : static_cast<double>(__ldcg(static_cast<const int *>(p.pos) + at));
-    const double turns = pos * p.freq[pair];
-    float s, cs;
-    sincospif(2.0f * static_cast<float>(turns - rint(turns)), &s, &cs);
-    turn[i] = make_float2(cs, p.inverse ? -s : s);
-  }
+  const double turns = (p.pos_float ? static_cast<double>(__int_as_float(raw)) : static_cast<double>(raw)) * pair_freq;
+  float sine, cosine;
+  sincospif(2.0f * static_cast<float>(turns - rint(turns)), &sine, &cosine);
+  turn[threadIdx.x] = make_float2(cosine, p.inverse ? -sine : sine);
   __syncthreads();
   // y0 = x0 c0 - x1 s1, y1 = x0 s0 + x1 c1: cos and sin, with the norm weight of the element they multiply
   float2 c0[2], s0[2], c1[2], s1[2];
@@ -204,9 +211,15 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rope_nd_kernel(const __grid_c
         sum = dev::fma2_rn(x1[1], x1[1], sum);
         scale[i] = sum.x + sum.y;
       }
-      for (int o = lanes >> 1; o > 0; o >>= 1)
+      if (round + UNROLL / 2 < rounds) {
+        for (int o = lanes >> 1; o > 0; o >>= 1)
 #pragma unroll
-        for (int i = 0; i < UNROLL; ++i) scale[i] += __shfl_xor_sync(0xFFFFFFFFu, scale[i], o);
+          for (int i = 0; i < UNROLL; ++i) scale[i] += __shfl_xor_sync(0xFFFFFFFFu, scale[i], o);
+      } else {                                // two heads are left
+        for (int o = lanes >> 1; o > 0; o >>= 1)
+#pragma unroll
+          for (int i = 0; i < UNROLL / 2; ++i) scale[i] += __shfl_xor_sync(0xFFFFFFFFu, scale[i], o);
+      }
 #pragma unroll
       for (int i = 0; i < UNROLL; ++i) scale[i] = normed ? rsqrtf(fmaf(scale[i], p.inv_d, p.eps)) : 1.0f;
     }
@@ -311,7 +324,7 @@ extern "C" int rope_nd(const rope_nd_tensor_t *Q, const rope_nd_tensor_t *K, int
   for (int i = 0; i < D / 2; ++i) {
     if (plan->axis[i] >= plan->axes) return fail(SVDQ_ERR_SHAPE, "rope_nd: a pair's axis is outside [0, axes)");
     p.axis[i] = plan->axis[i];
-    p.freq[i] = plan->freq[i] / 6.283185307179586;   // radians to turns
+    p.freq[i] = plan->freq[i] * 0.15915494309189535;   // radians to turns: / 2 pi
   }
   int rc = check_tensor("query", *Q, M, D);
   if (rc == SVDQ_OK && K) rc = check_tensor("key", *K, M, D);
@@ -343,8 +356,8 @@ extern "C" int rope_nd(const rope_nd_tensor_t *Q, const rope_nd_tensor_t *K, int
   p.eps = eps;
   p.inv_d = 1.0f / static_cast<float>(D);
   while ((1 << p.lanes_log2) < D / 8) ++p.lanes_log2;
-  // Groups per token: four, which with a block's tokens makes one angle a thread (more tokens a block would compute
-  // more); more while that leaves SMs without a block or two.  Each tensor's heads take a share of the groups by
+  // Groups per token: four, which with a block's tokens makes one angle a thread (eight: 21.4 us for 4608 normed rows x
+  // 40 heads x 128, and 7.6 us for 9000 rows x 4 heads x 64); more while that leaves SMs without a block or two.  Each tensor's heads take a share of the groups by
   // their number.
   const int hq = Q->heads, hk = K ? K->heads : 0, most = 7 - p.lanes_log2;   // log2 of a block's groups
   const auto blocks_at = [&](int g) {
@@ -360,8 +373,7 @@ extern "C" int rope_nd(const rope_nd_tensor_t *Q, const rope_nd_tensor_t *K, int
     p.q_groups = (groups * hq + (hq + hk) / 2) / (hq + hk);
     p.q_groups = p.q_groups < 1 ? 1 : p.q_groups > groups - 1 ? groups - 1 : p.q_groups;
   }
-  const size_t smem = (static_cast<size_t>(1) << (most - p.groups_log2)) * (D / 2) * sizeof(float2);
-  DependentLaunch dl(dim3(blocks_at(p.groups_log2)), dim3(THREADS), smem, stream);
+  DependentLaunch dl(dim3(blocks_at(p.groups_log2)), dim3(THREADS), 0, stream);
   const bool norm = Q->norm || (K && K->norm);
   cudaError_t e = plan->pairing == ROPE_ND_HALF
                       ? (norm ? cudaLaunchKernelEx(&dl.cfg, rope_nd_kernel<true, true>, p)
