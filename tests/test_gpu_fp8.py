@@ -448,3 +448,36 @@ def test_block_of_layers():
     g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(again, (h, q, k, o, p, u, y)))
+
+
+def gelu_sweep(N):
+    """N bf16 values: every one of 2^-8 <= |b| <= 13 on the negative side and <= 8 on the other, over and over."""
+    bits = torch.arange(0x3B80, 0x4151, dtype=torch.int16).view(torch.bfloat16)
+    every = torch.cat([-bits, bits[bits <= 8]])
+    return every.repeat(-(-N // len(every)))[:N]
+
+
+def close_gelu(got, y):
+    """GELU (erf) of exact arguments.  For y < 0 the result is y Phi(y), relative to which the kernel's polynomial for log2 Phi,
+    evaluated in float32 on a dense grid, is off by less than 6.1e-6 down to -2, 4.8e-5 down to -5 and 4.1e-4 down to -13, and
+    the exponential by 2^-22: 2^-17, 2^-14 and 2^-11 hold their sums.  For y >= 0 the result is y - y Phi(-y), of which no
+    more than half is subtracted: 2^-17.  Then bf16's half step; below 2^-121 Phi itself is no normal float32 and may count
+    as zero."""
+    got, want = G.bf16_host(got), fp8.gelu(y, 1)
+    rel = np.where(y >= -2, 2.0 ** -17, np.where(y >= -5, 2.0 ** -14, 2.0 ** -11))
+    bad = ~(np.abs(got - want) <= (2.0 ** -8 + 1.01 * rel) * np.abs(want) + 2.0 ** -121)
+    assert not bad.any(), (int(bad.sum()), y[bad][:6], got[bad][:6], want[bad][:6])
+
+
+@pytest.mark.parametrize("M,K,N", [(3, 136, 2992), (40, 136, 2992), (140, 136, 2992), (2600, 2056, 5640)])
+def test_gelu_erf_of_exact_arguments(M, K, N):
+    """Arguments that are exact in float32: a bias of every bf16 value beside one product, of a row's own.  The last size
+    takes the 256-row tiles."""
+    b = gelu_sweep(N)
+    shift = torch.arange(M) % 16 / 512                             # e4m3 values, exact beside any bias in 24 bits
+    X, W = torch.zeros(M, K, dtype=torch.bfloat16), torch.zeros(K, N, dtype=torch.bfloat16)
+    X[:, 5], W[5] = shift.to(torch.bfloat16), 1
+    Y = layer.FP8Linear(W.to(G.DEV), b.to(G.DEV), lib.EPILOGUE_GELU_ERF)(X.to(G.DEV))
+    G.check_ok()
+    rows = sorted({*range(min(M, 16)), M // 2, M - 1})
+    close_gelu(Y[rows], shift.double().numpy()[rows, None] + b.double().numpy())
