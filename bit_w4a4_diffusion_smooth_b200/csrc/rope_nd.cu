@@ -262,30 +262,61 @@ bool apart(int64_t row, int64_t head, int M, int heads, int D) {
   if (heads == 1) return row >= D;
   return row <= head ? row >= D && head / M >= row : head >= D && row / heads >= head;
 }
-// Whether a vector of `b` (Y's, `heads_b` of them in a row) shares an element with one of `a`, where both have the
-// same strides; what two tensors of different strides share is not looked for.
-bool overlap(const void *a, int64_t a_row, int64_t a_head, int heads_a, const void *b, int64_t b_row, int64_t b_head,
-             int heads_b, int M, int D) {
-  if ((M > 1 && a_row != b_row) || (heads_a > 1 && heads_b > 1 && a_head != b_head)) return a == b;
-  const int64_t delta = (static_cast<const uint8_t *>(b) - static_cast<const uint8_t *>(a)) / 2;
-  const int64_t head = heads_a > 1 ? a_head : b_head;
-  // m b_row + h head + d = delta, with |d| < D, m and h a difference of two rows and of two heads: the wider stride's
-  // factor is one of the two next to the quotient, then the other's
-  struct Dim {
-    int64_t step, lo, hi;
-  } wide = {M > 1 ? b_row : 0, 1 - M, M - 1}, near = {heads_a > 1 || heads_b > 1 ? head : 0, 1 - heads_b, heads_a - 1};
-  if (wide.step < near.step) std::swap(wide, near);
-  const auto quotient = [](int64_t n, const Dim &dim) {
-    return dim.step > 0 ? n / dim.step - (n % dim.step < 0) : 0;
+// Whether a vector of `b` (a Y's) shares an element with one of `a`.  Exact where both have the same strides and neither
+// overlaps itself; otherwise ranges that meet count as shared, unless the two lie beside one another in rows (or head
+// planes) of one stride, as the heads of a fused projection do.
+struct Heads {
+  const void *at;
+  int64_t row, head;
+  int heads;
+};
+bool overlap(const Heads &a, const Heads &b, int M, int D) {
+  const int64_t delta = (static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.at)) -
+                         static_cast<int64_t>(reinterpret_cast<uintptr_t>(a.at))) / 2;
+  // the elements of each, from its first address on: strides may be negative or 0 (an X's), and nothing bounds them
+  struct Range {
+    __int128 lo, hi;
   };
-  const int64_t i0 = quotient(delta, wide);
-  for (int64_t i = i0; i <= i0 + 1; ++i) {
-    if (i < wide.lo || i > wide.hi) continue;
-    const int64_t rest = delta - i * wide.step, j0 = quotient(rest, near);
-    for (int64_t j = j0; j <= j0 + 1; ++j)
-      if (j >= near.lo && j <= near.hi && std::abs(rest - j * near.step) < D) return true;
+  const auto range = [&](const Heads &t) {
+    const __int128 rows = static_cast<__int128>(t.row) * (M - 1), heads = static_cast<__int128>(t.head) * (t.heads - 1);
+    return Range{(rows < 0 ? rows : 0) + (heads < 0 ? heads : 0), (rows > 0 ? rows : 0) + (heads > 0 ? heads : 0) + D};
+  };
+  const Range ra = range(a), rb = range(b);
+  if (rb.lo + delta >= ra.hi || ra.lo >= rb.hi + delta) return false;
+  const bool one_row = M == 1 || a.row == b.row, one_head = a.heads == 1 || b.heads == 1 || a.head == b.head;
+  if (one_row && one_head && apart(a.row, a.head, M, a.heads, D)) {
+    const int64_t head = a.heads > 1 ? a.head : b.head;
+    // m row + h head + d = delta, with |d| < D, m and h a difference of two rows and of two heads: the wider stride's
+    // factor is one of the two next to the quotient, then the other's
+    struct Dim {
+      int64_t step, lo, hi;
+    } wide = {M > 1 ? b.row : 0, 1 - M, M - 1}, near = {a.heads > 1 || b.heads > 1 ? head : 0, 1 - b.heads, a.heads - 1};
+    if (wide.step < near.step) std::swap(wide, near);
+    const auto quotient = [](int64_t n, const Dim &dim) {
+      return dim.step > 0 ? n / dim.step - (n % dim.step < 0) : 0;
+    };
+    const int64_t i0 = quotient(delta, wide);
+    for (int64_t i = i0; i <= i0 + 1; ++i) {
+      if (i < wide.lo || i > wide.hi) continue;
+      const int64_t rest = delta - i * wide.step, j0 = quotient(rest, near);
+      for (int64_t j = j0; j <= j0 + 1; ++j)
+        if (j >= near.lo && j <= near.hi && std::abs(rest - j * near.step) < D) return true;
+    }
+    return false;
   }
-  return false;
+  // each a run of `run` elements, and those `period` apart: beside one another if the second's place in the first's
+  // period is behind the first's run and ends before the next
+  const auto beside = [&](int64_t period, __int128 run_a, __int128 run_b) {
+    if (period <= 0) return false;
+    const int64_t place = (delta % period + period) % period;
+    return place >= run_a && place + run_b <= period;
+  };
+  const auto run = [&](int64_t step, int n) { return static_cast<__int128>(step) * (n - 1) + D; };
+  if (M > 1 && a.row == b.row && (a.heads == 1 || a.head >= 0) && (b.heads == 1 || b.head >= 0) &&
+      beside(a.row, run(a.heads > 1 ? a.head : 0, a.heads), run(b.heads > 1 ? b.head : 0, b.heads)))
+    return false;
+  return !(a.heads > 1 && b.heads > 1 && a.head == b.head && (M == 1 || (a.row >= 0 && b.row >= 0)) &&
+           beside(a.head, run(M > 1 ? a.row : 0, M), run(M > 1 ? b.row : 0, M)));
 }
 int check_tensor(const char *which, const rope_nd_tensor_t &t, int M, int D) {
   const std::string name = std::string("rope_nd: ") + which;
@@ -333,8 +364,8 @@ extern "C" int rope_nd(const rope_nd_tensor_t *Q, const rope_nd_tensor_t *K, int
     return fail(SVDQ_ERR_INVALID_ARG, "rope_nd: the inverse undoes the turn only and takes no norm");
   if (reinterpret_cast<uintptr_t>(pos) & 3u) return fail(SVDQ_ERR_ALIGNMENT, "rope_nd: pos must be 4-byte aligned");
   const auto shared = [&](const rope_nd_tensor_t &a, bool out, const rope_nd_tensor_t &b) {   // a's X or Y and b's Y
-    return out ? overlap(a.Y, a.y_row, a.y_head, a.heads, b.Y, b.y_row, b.y_head, b.heads, M, D)
-               : overlap(a.X, a.x_row, a.x_head, a.heads, b.Y, b.y_row, b.y_head, b.heads, M, D);
+    return overlap(out ? Heads{a.Y, a.y_row, a.y_head, a.heads} : Heads{a.X, a.x_row, a.x_head, a.heads},
+                   Heads{b.Y, b.y_row, b.y_head, b.heads}, M, D);
   };
   if ((Q->X != Q->Y && shared(*Q, false, *Q)) ||
       (K && ((K->X != K->Y && shared(*K, false, *K)) || shared(*Q, false, *K) || shared(*K, false, *Q) || shared(*Q, true, *K))))

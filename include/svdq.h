@@ -640,7 +640,9 @@ typedef struct rope_nd_tensor {
  * 1 <= heads <= 65535; strides multiples of 8; pointers 16-byte aligned (pos
  * 4-byte); pos_row >= 0 (0: one position for all rows); the heads of a Y must
  * not overlap one another, the other Y, the other tensor's X, or its own X
- * unless it is that X (checked where the strides are the same).
+ * unless it is that X.  Where two of them have different strides, or an X
+ * overlaps itself, they count as overlapping if their ranges do, unless they
+ * lie beside one another in rows (or head planes) of one stride.
  */
 int rope_nd(const rope_nd_tensor_t *Q, const rope_nd_tensor_t *K, int M, const rope_nd_plan_t *plan, const void *pos,
             int64_t pos_row, int pos_is_float, int inverse, float eps, svdq_stream_t stream);

@@ -169,3 +169,66 @@ def test_sizes_past_a_c_int_are_refused_not_cut_down():
         with pytest.raises(ValueError):
             lib._c_int(n, "rows")
     assert lib._c_int(2 ** 31 - 1, "rows") == 2 ** 31 - 1
+
+
+def _span(X, row, head, heads, M, D=16):
+    c = _cells(X, row, head, heads, M, D)
+    return min(c), max(c)
+
+
+def test_rope_refuses_shared_elements_under_other_strides():
+    """Tensors whose strides differ: what shares an element is refused, what lies in ranges of its own or beside the
+    other in rows of one stride is taken."""
+    if torch.cuda.is_available():
+        pytest.skip("the accepted calls would run")
+    M, seen = 3, {"shared": 0, "apart": 0, "beside": 0}
+    layouts = [(96, 16, 2), (96, 32, 2), (64, 16, 4), (16, 48, 2), (32, 96, 2), (32, 128, 2), (0, 16, 2), (16, 0, 2),
+               (96, 48, 1), (32, 16, 4)]
+    for xrow, xhead, heads in layouts:
+        for yrow, yhead, n in layouts:
+            if (xrow, xhead) == (yrow, yhead) or n != heads or not (yrow >= 96 and yhead <= 32 or yhead >= 48 and yrow):
+                continue
+            for off in range(-400, 400, 8):
+                X, Y = 4096, 4096 + 2 * off
+                if X == Y:
+                    continue
+                x, y = _cells(X, xrow, xhead, heads, M), _cells(Y, yrow, yhead, heads, M)
+                if len(y) != M * heads * 16:                    # a Y that overlaps itself is refused for that
+                    continue
+                rc = _rope(q=(X, xrow, xhead, Y, yrow, yhead, None, heads), M=M)
+                (x0, x1), (y0, y1) = _span(X, xrow, xhead, heads, M), _span(Y, yrow, yhead, heads, M)
+                if x & y:
+                    seen["shared"] += 1
+                    assert rc == lib.ERR_INVALID_ARG, (xrow, xhead, yrow, yhead, heads, off)
+                elif x0 > y1 or y0 > x1:
+                    seen["apart"] += 1
+                    assert rc == lib.ERR_NOT_INITIALIZED, (xrow, xhead, yrow, yhead, heads, off)
+                elif xrow == yrow and (y0 - x0) % xrow >= (heads - 1) * xhead + 16 and \
+                        (y0 - x0) % xrow + (heads - 1) * yhead + 16 <= xrow:
+                    seen["beside"] += 1
+                    assert rc == lib.ERR_NOT_INITIALIZED, (xrow, xhead, yrow, yhead, heads, off)
+    assert min(seen.values()) >= 10, seen
+
+
+def test_rope_refuses_an_output_inside_the_projection_it_reads():
+    """A contiguous output viewed at an offset into the fused projection's buffer: other strides, shared elements."""
+    M, H, D, row = 6, 2, 16, 3 * 2 * 16
+    fused, k = 4096, 4096 + 2 * H * D
+    q = (fused, row, D, fused + 2 * row, H * D, D, None, H)
+    assert _rope(q=q, k=(k, row, D, 65536, row, D, None, H), M=M) == lib.ERR_INVALID_ARG
+    # the query's output on the keys, the keys' on the queries
+    q = (fused, row, D, k + 2 * row, H * D, D, None, H)
+    assert _rope(q=q, k=(k, row, D, 65536, row, D, None, H), M=M) == lib.ERR_INVALID_ARG
+    # windows of rows that overlap one another, and an output on the last of them
+    q = (4096, 32, 16, 65536, 96, 16, None, 6)
+    assert _rope(q=q, k=(32768, 32, 16, 4096 + 2 * 112, 32, 16, None, 2), M=2) == lib.ERR_INVALID_ARG
+    if not torch.cuda.is_available():
+        # in place beside values between the key heads: other head strides in rows of one stride
+        row = 8 * 16
+        q = (4096, row, 16, 4096, row, 16, None, 4)
+        kv = (4096 + 2 * 64, row, 32, 4096 + 2 * 64, row, 32, None, 2)
+        assert _rope(q=q, k=kv, M=M) == lib.ERR_NOT_INITIALIZED
+        # and the same by heads: planes of one stride, rows of others
+        q = (4096, 16, 512, 4096, 16, 512, None, 2)
+        kv = (4096 + 2 * 256, 32, 512, 4096 + 2 * 256, 32, 512, None, 2)
+        assert _rope(q=q, k=kv, M=M) == lib.ERR_NOT_INITIALIZED
