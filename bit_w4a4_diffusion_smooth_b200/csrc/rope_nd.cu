@@ -9,11 +9,16 @@
 //
 // Angles are taken in float64: a float32 product pos * f is off by up to
 // pos 2^-24 radians, which at positions in the ten thousands is already bf16's
-// own step.  They are counted in turns, so that the whole turns come off with
-// one rounding; what is left, within half a turn, goes to float32 (off by at
-// most 2^-26 turns), and its cosine and sine are float32 like everything else,
-// rounded once to bf16.  (Float64 cosines and sines gave no other bits that
-// count and took 0.3 us more for 4608 rows.)  A block computes each of its tokens'
+// own step.  They are counted in turns, with what the two products' roundings
+// left out carried along, so that the whole turns come off right at any
+// position; what is left, within half a turn, goes to float32, whose cosine and
+// sine take the rest (up to 2^-26 turns) as a first-order term.  Both are then
+// off by 3 * 2^-24 of their own value at most (a unit in the last place of
+// sincospif and the term's rounding), next to a quarter turn too, where a
+// rounded angle would lose a small cosine whole; everything else is float32,
+// rounded once to bf16.  (Without the two terms: 0.1 us of 18.8 less for 4608
+// normed rows x 40 heads x 128, 4.5 us against 4.7 for 9000 rows x 4 heads x
+// 64.)  A block computes each of its tokens'
 // D/2 angles once, into shared memory, and every head of those tokens uses
 // them, so the call needs no table in memory and no launch to fill one.
 //
@@ -24,8 +29,8 @@
 // tensor, in registers and walks over that tensor's heads, four heads' loads in
 // flight at a time, each place loaded again as soon as its head is turned; the
 // first four are under way while the block computes its angles.  64 registers
-// let 8 blocks share an SM (4608 normed rows x 40 heads x 128: 18.6 us; 20.2
-// with 7, 22.8 with 9, which spill).  The arithmetic runs on f32x2 instructions, two pairs at once: with
+// let 8 blocks share an SM (4608 normed rows x 40 heads x 128: 18.8 us; 1.6
+// more with 7, 4.2 with 9, which spill).  The arithmetic runs on f32x2 instructions, two pairs at once: with
 // scalar ones, and the tensor chosen head by head, the normed call was bound by
 // issue (30 us for those rows).
 #include <cuda_runtime.h>
@@ -44,6 +49,8 @@ namespace {
 constexpr int THREADS = 128;
 constexpr int BLOCKS = 8;         // on an SM
 constexpr int MAX_D = 256;
+// 1 / 2 pi as the sum of two float64
+constexpr double PER_RADIAN = 0.15915494309189535, PER_RADIAN_LOW = -9.839338337591243e-18;
 static_assert(4 * (MAX_D / 8) <= THREADS, "a token's heads go to four groups of lanes at least");
 
 struct Tensor {
@@ -62,7 +69,7 @@ struct Params {
   int q_groups;                 // of which the first so many take the query's heads
   int pos_float, inverse;
   float eps, inv_d;
-  double freq[MAX_D / 2];       // turns per position
+  double freq[MAX_D / 2];       // radians per position
   unsigned char axis[MAX_D / 2];
 };
 
@@ -123,7 +130,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rope_nd_kernel(const __grid_c
   const int m0 = static_cast<int>(blockIdx.x) * tokens;
   // A thread has at most one angle: with four groups a token or more, tokens D / 2 <= THREADS.  Its pair's axis and
   // frequency are loaded through generic addresses: as constants, which the compiler would read them as, a warp's 32
-  // pairs took 32 accesses one after the other (9000 rows x 4 heads x 64: 7.8 us against 4.5).
+  // pairs took 32 accesses one after the other (9000 rows x 4 heads x 64: 3.3 us more).
   const int a_tok = static_cast<int>(threadIdx.x) / half_d, pair = static_cast<int>(threadIdx.x) % half_d;
   const double *freq = p.freq;
   const unsigned char *axis = p.axis;
@@ -168,9 +175,19 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) rope_nd_kernel(const __grid_c
   if constexpr (NORM)
     if (on && normed) load8<HALF>(t.norm, c, p.D, nw);
 
-  const double turns = (p.pos_float ? static_cast<double>(__int_as_float(raw)) : static_cast<double>(raw)) * pair_freq;
+  // The frequency in turns and the position's product with it, each with what its rounding left out; then whole turns off.
+  // (Where even a unit in the last place is whole turns, the second remainder keeps the angle within half a turn.)
+  const double per = pair_freq * PER_RADIAN, per_low = fma(pair_freq, PER_RADIAN, -per) + pair_freq * PER_RADIAN_LOW;
+  const double at = p.pos_float ? static_cast<double>(__int_as_float(raw)) : static_cast<double>(raw);
+  const double turns = at * per, turns_low = fma(at, per_low, fma(at, per, -turns));
+  double rest = (turns - rint(turns)) + turns_low;
+  rest -= rint(rest);
+  const float near = static_cast<float>(rest), off = static_cast<float>(rest - static_cast<double>(near)) * 6.2831853f;
   float sine, cosine;
-  sincospif(2.0f * static_cast<float>(turns - rint(turns)), &sine, &cosine);
+  sincospif(2.0f * near, &sine, &cosine);
+  const float sine_near = sine;
+  sine = fmaf(cosine, off, sine);
+  cosine = fmaf(-sine_near, off, cosine);
   turn[threadIdx.x] = make_float2(cosine, p.inverse ? -sine : sine);
   __syncthreads();
   // y0 = x0 c0 - x1 s1, y1 = x0 s0 + x1 c1: cos and sin, with the norm weight of the element they multiply
@@ -355,7 +372,7 @@ extern "C" int rope_nd(const rope_nd_tensor_t *Q, const rope_nd_tensor_t *K, int
   for (int i = 0; i < D / 2; ++i) {
     if (plan->axis[i] >= plan->axes) return fail(SVDQ_ERR_SHAPE, "rope_nd: a pair's axis is outside [0, axes)");
     p.axis[i] = plan->axis[i];
-    p.freq[i] = plan->freq[i] * 0.15915494309189535;   // radians to turns: / 2 pi
+    p.freq[i] = plan->freq[i];
   }
   int rc = check_tensor("query", *Q, M, D);
   if (rc == SVDQ_OK && K) rc = check_tensor("key", *K, M, D);

@@ -210,3 +210,66 @@ def test_rows_past_32_bit_offsets():
     rows = torch.tensor([0, 16, 65535, 65536, 65537, M - 1], device=G.DEV)
     assert M * H * D * 2 > 2 ** 31
     close(out[rows], x[rows], pos[rows], [128], False)
+
+
+# Error of the kernel's turn, before bf16: the angle's product with the frequency and its remainder within half a turn are
+# float64 with their rounding errors carried (2^-50 of a radian for any position), its float32 remainder's own error (up to
+# 2^-26 turns) goes back into cosine and sine as a first-order term (what that leaves out: below 2^-46), sincospif is off by
+# one unit in the last place at most (2^-23 of the value), and that correction, the product and the sum round once each
+# (2^-24).  Of x cos - y sin that is 6 * 2^-24 of |x cos| + |y sin| <= |x| + |y|, plus 2^-45 of it.
+
+def extended(x, pos, turn, half, inverse=False):
+    """(x, y) turned in 80-bit arithmetic by the frequencies of the layer's plan; and |x cos| + |y sin|."""
+    x, pos = f64(x), f64(pos).astype(np.longdouble)
+    n = x.shape[-1] // 2
+    freq = np.array(turn.plan.freq[:n], dtype=np.longdouble)
+    angle = (pos[:, np.array(turn.plan.axis[:n], dtype=np.int64)] * freq)[:, None, :] * (-1 if inverse else 1)
+    c, s = np.cos(angle), np.sin(angle)
+    a, b = (x[..., :n], x[..., n:]) if half else (x[..., 0::2], x[..., 1::2])
+    join = lambda u, v: np.concatenate([u, v], -1) if half else np.stack([u, v], -1).reshape(x.shape)
+    return join(a * c - b * s, a * s + b * c), join(abs(a * c) + abs(b * s), abs(a * s) + abs(b * c))
+
+
+def close_extended(got, x, pos, turn, half, inverse=False):
+    want, mag = extended(x, pos, turn, half, inverse)
+    d = 6 * 2.0 ** -24 * mag + 2.0 ** -45 * (1 + mag)
+    bad = ~(np.abs(f64(got) - want) <= d + 2.0 ** -8 * (np.abs(want) + d) + 2.0 ** -134)
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4].tolist(), f64(got)[bad][:4], want[bad][:4])
+
+
+@pytest.mark.parametrize("half", [False, True])
+def test_angles_next_to_a_quarter_turn(half):
+    """Where a cosine or a sine is small its value is the angle's distance from the quarter turns: float32 positions next
+    to odd and even multiples of pi / 2, and whole ones that come near them, turning (1, 0)."""
+    k = torch.arange(1, 700, dtype=torch.float64)
+    near = (k * (np.pi / 2)).float()
+    pos = torch.cat([near, torch.nextafter(near, torch.tensor(0.0)), -near,
+                     torch.tensor([11., 22., 355., 710., 52174., 103993., 104348., 208341., 5419351.])])[:, None].to(G.DEV)
+    x = torch.zeros(pos.shape[0], 1, 8, dtype=torch.bfloat16, device=G.DEV)
+    x[..., 0] = 1
+    turn = layer.RotaryND([8], interleaved=not half)
+    for inverse in (False, True):
+        got = turn(x, None, pos, inverse=inverse)[0]
+        G.check_ok()
+        close_extended(got, x, pos, turn, half, inverse)
+
+
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("kind", ["int", "fraction", "large float"])
+def test_far_positions_keep_their_angles(half, kind):
+    r = np.random.default_rng(5)
+    axes, M = [32, 64, 32], 300
+    pos = {"int": r.integers(-2 ** 31, 2 ** 31, size=(M, 3)).astype(np.int32),
+           "fraction": (r.random((M, 3)) * 2e6 - 1e6).astype(np.float32),
+           "large float": (r.normal(size=(M, 3)) * 2.0 ** 40).astype(np.float32)}[kind]
+    if kind == "int":
+        pos[0], pos[1], pos[2] = -2 ** 31, 2 ** 31 - 1, 0
+    pos, x = torch.from_numpy(pos).to(G.DEV), rand(6, M, 2, 128)
+    turn = layer.RotaryND(axes, interleaved=not half)
+    got = turn(x, None, pos)[0]
+    G.check_ok()
+    if kind == "large float":           # the 80-bit product of 2^42 is itself off by 2^-22
+        want, mag = extended(x, pos, turn, half)
+        assert (np.abs(f64(got) - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -20 * (1 + mag)).all()
+    else:
+        close_extended(got, x, pos, turn, half)
