@@ -232,3 +232,35 @@ def test_rope_refuses_an_output_inside_the_projection_it_reads():
         q = (4096, 16, 512, 4096, 16, 512, None, 2)
         kv = (4096 + 2 * 256, 32, 512, 4096 + 2 * 256, 32, 512, None, 2)
         assert _rope(q=q, k=kv, M=M) == lib.ERR_NOT_INITIALIZED
+
+
+def _meta(shape, stride):
+    return torch.empty_strided(shape, stride, dtype=torch.bfloat16, device="meta")
+
+
+def test_layer_refuses_sizes_past_a_c_int():
+    """The layer's own check, on tensors without memory: 2^31 rows, and row strides of 2^31 and 2^32 + 64."""
+    lin = layer.FP8Linear.__new__(layer.FP8Linear)
+    lin.K, lin.N, lin.device, lin.bias = 64, 64, torch.device("meta"), None
+    ok = _meta((2, 64), (64, 1))
+    for X, Y in ((_meta((2 ** 31, 64), (64, 1)), None), (_meta((2, 64), (2 ** 31, 1)), None),
+                 (_meta((2, 64), (2 ** 32 + 64, 1)), None), (ok, _meta((2, 64), (2 ** 31, 1))),
+                 (ok, _meta((2, 64), (2 ** 32 + 64, 1)))):
+        with pytest.raises(ValueError, match="too large"):
+            lin._call(X, None, Y, 0)
+
+
+def test_library_calls_refuse_sizes_past_a_c_int():
+    packed = torch.empty(lib.fp8_weight_size(64, 64), dtype=torch.uint8)
+    many, wide = _meta((2 ** 31, 64), (64, 1)), _meta((2, 2 ** 32 + 64), (2 ** 32 + 64, 1))
+    off = torch.zeros(2, dtype=torch.int32)
+    for X in (many, wide):
+        with pytest.raises(ValueError, match="too large"):
+            lib.fp8_linear(X, packed, None, 64, 0, 0, X)
+        with pytest.raises(ValueError, match="too large"):
+            lib.fp8_linear_grouped(X, off, packed, None, 64, 0, 0, X)
+    for W in (_meta((64, 2 ** 31), (2 ** 31, 1)), _meta((2 ** 32 + 64, 64), (64, 1))):
+        with pytest.raises(ValueError, match="too large"):
+            lib.fp8_pack_weights(W)
+    with pytest.raises(ValueError):
+        lib.fp8_pack_weights(W[0])

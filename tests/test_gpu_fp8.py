@@ -481,3 +481,45 @@ def test_gelu_erf_of_exact_arguments(M, K, N):
     G.check_ok()
     rows = sorted({*range(min(M, 16)), M // 2, M - 1})
     close_gelu(Y[rows], shift.double().numpy()[rows, None] + b.double().numpy())
+
+
+@pytest.mark.parametrize("M", [1, 16, 40, 300])
+def test_library_calls_equal_the_layers(M):
+    """fp8_pack_weights, fp8_linear and fp8_linear_grouped by their bindings, with workspaces of the caller's."""
+    K, N, E = 264, 136, 2
+    w, b = bf16(rand(1, E, K, N, scale=0.05, loud=False)).to(G.DEV), bf16(rand(2, E, N, loud=False)).to(G.DEV)
+    x = bf16(rand(3, M, K + 8)).to(G.DEV)[:, :K]
+    need = lib.fp8_workspace_size(M, K)
+    ws = G.poisoned_u8(need) if need else None
+    Y = G.poisoned_bf16(M + 1, N + 8)
+    lib.fp8_linear(x, lib.fp8_pack_weights(w[0]), b[0], N, lib.EPILOGUE_GELU_TANH, 40, Y[:M, :N], workspace=ws)
+    assert torch.equal(Y[:M, :N], layer.FP8Linear(w[0], b[0], lib.EPILOGUE_GELU_TANH, 40)(x))
+    assert torch.isnan(Y[M]).all() and torch.isnan(Y[:, N:]).all()
+    need = lib.fp8_workspace_size(M, K, E)
+    ws = G.poisoned_u8(need) if need else None
+    packed = G.poisoned_u8(lib.fp8_weight_size(K, N, E) + 16)
+    assert lib.fp8_pack_weights(w, packed[:-16]) is not None and (packed[-16:] == G.POISON).all()
+    off = torch.tensor([0, M // 3, M], dtype=torch.int32, device=G.DEV)
+    Y = G.poisoned_bf16(M + 1, N)
+    lib.fp8_linear_grouped(x, off, packed, b, N, lib.EPILOGUE_NONE, 0, Y[:M], workspace=ws)
+    assert torch.equal(Y[:M], layer.FP8Experts(w, b)(x, off)) and torch.isnan(Y[M]).all()
+    G.check_ok()
+
+
+def test_library_calls_refuse():
+    M, K, N = 40, 264, 136
+    w, x = (torch.zeros(*s, dtype=torch.bfloat16, device=G.DEV) for s in ((K, N), (M, K)))
+    packed, ws = lib.fp8_pack_weights(w), G.poisoned_u8(lib.fp8_workspace_size(M, K))
+    Y, off = G.poisoned_bf16(M, N), torch.tensor([0, M], dtype=torch.int32, device=G.DEV)
+    b = torch.zeros(N, dtype=torch.bfloat16, device=G.DEV)
+    lin = lambda x=x, p=packed, b=b, Y=Y, ws=ws: lib.fp8_linear(x, p, b, N, 0, 0, Y, workspace=ws)
+    ex = lambda off=off, b=b, Y=Y, ws=ws: lib.fp8_linear_grouped(x, off, packed, b, N, 0, 0, Y, workspace=ws)
+    for call in (lambda: lin(ws=None), lambda: lin(ws=ws[:-1]), lambda: lin(p=packed[:-1]), lambda: lin(b=b[:-1]),
+                 lambda: lin(Y=Y[:-1]), lambda: lin(Y=Y[:, :-8]), lambda: lin(x=x.float()), lambda: lin(x=x.cpu()),
+                 lambda: lin(x=torch.zeros(K, M, dtype=torch.bfloat16, device=G.DEV).T), lambda: lin(b=b.float()),
+                 lambda: ex(ws=None), lambda: ex(off=off.long()), lambda: ex(off=off.cpu()), lambda: ex(b=b[:-1]),
+                 lambda: ex(off=off[:, None]), lambda: ex(Y=Y[:-1]),
+                 lambda: ex(off=torch.zeros(4, dtype=torch.int32, device=G.DEV)[::2])):
+        with pytest.raises(ValueError):
+            call()
+    assert torch.isnan(Y).all()
