@@ -523,3 +523,59 @@ def test_library_calls_refuse():
         with pytest.raises(ValueError):
             call()
     assert torch.isnan(Y).all()
+
+
+# Few column tiles and a long K: the few-row kernel splits K over clusters of 2 (from 8 blocks of 128 on), 4 (16) and 8 (32)
+# CTAs, here with an odd number of two-block stages and a last stage of one block as well.
+SPLIT_K = [1024, 1032, 2048, 2184, 4096, 4104, 4352, 5000]
+
+
+@pytest.mark.parametrize("M", [1, 2, 15, 16, 17, 20, 32, 50, 64, 100, 128])
+@pytest.mark.parametrize("N", [8, 136, 512])
+def test_long_k_split_over_clusters(M, N):
+    r = np.random.default_rng(M + N)
+    for K in SPLIT_K:
+        x, w = r.integers(-8, 9, size=(M, K)).astype(float), r.integers(-8, 9, size=(K, N)).astype(float)
+        b = r.integers(-100, 101, size=N).astype(float)
+        Y, Yf = run_linear(x, w, b, ldy=N + 8)
+        assert torch.equal(Y.cpu(), bf16(x @ w + b)), K            # exact sums below 2^24
+        assert torch.isnan(Yf[:, N:]).all(), K
+
+
+@pytest.mark.parametrize("M", [1, 16, 20, 50, 100])
+@pytest.mark.parametrize("K,epilogue", [(1032, 2), (2184, 1), (4104, 0), (4104, 1)])
+def test_long_k_split_against_oracle_and_repeats(M, K, epilogue):
+    N = 264
+    x, w, b = rand(M, M, K), rand(K, K, N, scale=0.02, loud=False), rand(N, N, loud=False)
+    want, mag = fp8.linear(x, w, b, epilogue, 100)
+    lin = layer.FP8Linear(bf16(w).to(G.DEV), bf16(b).to(G.DEV), epilogue, 100)
+    X = bf16(x).to(G.DEV)
+    Y = lin(X)
+    close(Y, want, mag, K, epilogue)
+    for _ in range(5):
+        assert torch.equal(lin(X), Y)
+    G.check_ok()
+
+
+@pytest.mark.parametrize("counts,start,tail", [
+    ([0, 2, 0, 3], 1, 2), ([1], 0, 0), ([0, 0, 0], 2, 3), ([5, 0, 0, 0, 0, 0], 0, 0),     # 16-row tiles, X quantized inside
+    ([3, 17], 0, 0), ([0, 19], 1, 0), ([13, 40], 2, 1), ([30, 60], 0, 5), ([0, 100], 3, 0)])
+@pytest.mark.parametrize("N", [8, 200])
+def test_experts_with_a_long_k(counts, start, tail, N):
+    """Splits by expert: clusters without a unit of work (empty experts, rows of no expert), tiles that begin behind a
+    multiple of 8 rows, repeats bit for bit."""
+    r = np.random.default_rng(sum(counts) + N)
+    E, T = len(counts), start + sum(counts) + tail
+    off = start + np.concatenate([[0], np.cumsum(counts)])
+    live = np.zeros(T, bool)
+    live[off[0]:off[-1]] = True
+    for K in (1032, 2048, 4104, 4352):
+        x, w = r.integers(-8, 9, size=(T, K)).astype(float), r.integers(-8, 9, size=(E, K, N)).astype(float)
+        b = r.integers(-100, 101, size=(E, N)).astype(float)
+        Y = run_experts(x, w, off.tolist(), b)
+        want = np.full((T, N), np.nan)
+        for e in range(E):
+            want[off[e]:off[e + 1]] = x[off[e]:off[e + 1]] @ w[e] + b[e]
+        assert torch.equal(Y.cpu()[live], bf16(want[live])) and torch.isnan(Y.cpu()[~live]).all(), K
+        again = run_experts(x, w, off.tolist(), b)
+        assert torch.equal(again[live], Y[live])
