@@ -579,3 +579,59 @@ def test_experts_with_a_long_k(counts, start, tail, N):
         assert torch.equal(Y.cpu()[live], bf16(want[live])) and torch.isnan(Y.cpu()[~live]).all(), K
         again = run_experts(x, w, off.tolist(), b)
         assert torch.equal(again[live], Y[live])
+
+
+@pytest.mark.parametrize("counts,start,tail", [([1500, 0, 257, 1, 2000, 903], 0, 5), ([0, 700, 9, 2500, 1101], 13, 40)])
+def test_experts_on_the_256_row_tiles(counts, start, tail):
+    """Rows enough, and a K long enough, for the SM pairs: ragged and empty experts, first rows that are no multiple of 8,
+    bias rows of their own, exact sums."""
+    g = torch.Generator(device=G.DEV).manual_seed(sum(counts))
+    E, T, K, N = len(counts), start + sum(counts) + tail, 2056, 5000
+    ints = lambda *s: torch.randint(-8, 9, s, generator=g, device=G.DEV).to(torch.bfloat16)
+    x, w, b = ints(T, K), ints(E, K, N), ints(E, N)
+    off = start + np.concatenate([[0], np.cumsum(counts)])
+    Y = G.poisoned_bf16(T, N)
+    ex = layer.FP8Experts(w, b)
+    ex(x, torch.tensor(off, dtype=torch.int32, device=G.DEV), Y)
+    G.check_ok()
+    for e in range(E):
+        rows = slice(int(off[e]), int(off[e + 1]))
+        assert torch.equal(Y[rows], (x[rows].double() @ w[e].double() + b[e].double()).to(torch.bfloat16)), e
+    assert torch.isnan(Y[:off[0]]).all() and torch.isnan(Y[off[-1]:]).all()
+
+
+@pytest.mark.parametrize("epilogue", EPI[1:])
+def test_gelu_of_experts_on_the_256_row_tiles(epilogue):
+    """Each expert's own bias row and a column where the GELU begins, inside a run of 16 columns, on the SM pairs."""
+    counts, K, N, begin = [1500, 0, 257, 1, 2000, 903], 2056, 5000, 1003
+    E, T = len(counts), sum(counts)
+    b = torch.stack([gelu_sweep(N).roll(100 * e) for e in range(E)])
+    x, w = torch.zeros(T, K, dtype=torch.bfloat16), torch.zeros(E, K, N, dtype=torch.bfloat16)
+    x[:, 7], w[:, 7] = (torch.arange(T) % 16 / 512).to(torch.bfloat16), 1
+    off = np.concatenate([[0], np.cumsum(counts)])
+    Y = G.poisoned_bf16(T, N)
+    layer.FP8Experts(w.to(G.DEV), b.to(G.DEV), epilogue, begin)(
+        x.to(G.DEV), torch.tensor(off, dtype=torch.int32, device=G.DEV), Y)
+    G.check_ok()
+    for row in (0, 1, 1499, 1500, 1756, 1757, 1758, 3757, 3758, T - 1):
+        e = int(np.searchsorted(off, row, side="right")) - 1
+        y = float(x[row, 7]) + b[e].double().numpy()
+        assert torch.equal(Y[row, :begin].cpu(), torch.from_numpy(y[:begin]).to(torch.bfloat16)), row
+        if epilogue == lib.EPILOGUE_GELU_ERF:
+            close_gelu(Y[row:row + 1, begin:], y[None, begin:])
+        else:
+            close(Y[row:row + 1, begin:], fp8.gelu(y[None, begin:], 2), np.abs(y[None, begin:]), K, 2)
+
+
+@pytest.mark.parametrize("epilogue", EPI[1:])
+def test_gelu_and_nan_on_the_256_row_tiles(epilogue):
+    M, K, N = 2600, 2056, 5640
+    x, w = np.zeros((M, K)), np.zeros((K, N))
+    x[:, 0], w[0, 0::2], w[0, 1::2] = 64.0, 4.0, -4.0         # 256 and -256
+    x[M - 1, 5], x[300, 2000] = np.nan, np.inf
+    Y, Yf = run_linear(x, w, None, epilogue, ldy=N + 8)
+    bad = [300, M - 1]
+    assert torch.isnan(Y[bad]).all() and torch.isnan(Yf[:, N:]).all()
+    keep = torch.ones(M, dtype=torch.bool, device=G.DEV)
+    keep[bad] = False
+    assert (Y[keep][:, 0::2] == 256).all() and (Y[keep][:, 1::2] == 0).all()
