@@ -635,3 +635,23 @@ def test_gelu_and_nan_on_the_256_row_tiles(epilogue):
     keep = torch.ones(M, dtype=torch.bool, device=G.DEV)
     keep[bad] = False
     assert (Y[keep][:, 0::2] == 256).all() and (Y[keep][:, 1::2] == 0).all()
+
+
+@pytest.mark.parametrize("M,K,N", [(3, 136, 2992), (40, 136, 2992), (140, 136, 2992), (2600, 2056, 5640)])
+def test_gelu_tanh_of_exact_arguments(M, K, N):
+    """y / (1 + 2^x), x = -2 z log2 e: three float32 roundings of x (3 * 2^-24 |x| ln 2 of the exponential, |x| below 5.5 down
+    to y = -2, 25 to -5, 134 further on), the exponential and the reciprocal 2^-22 each, sum and product 2^-24 each, are less
+    than 2^-18, 2^-17 and 2^-15 of the result; the reciprocal is no normal float32 below 2^-121."""
+    b = gelu_sweep(N)
+    shift = torch.arange(M) % 16 / 512
+    X, W = torch.zeros(M, K, dtype=torch.bfloat16), torch.zeros(K, N, dtype=torch.bfloat16)
+    X[:, 5], W[5] = shift.to(torch.bfloat16), 1
+    Y = layer.FP8Linear(W.to(G.DEV), b.to(G.DEV), lib.EPILOGUE_GELU_TANH)(X.to(G.DEV))
+    G.check_ok()
+    rows = sorted({*range(min(M, 16)), M // 2, M - 1})
+    y = shift.double().numpy()[rows, None] + b.double().numpy()
+    want = y / (1 + np.exp(-2 * np.sqrt(2 / np.pi) * (y + 0.044715 * y ** 3)))     # without 1 + tanh's cancellation
+    rel = np.where(y >= -2, 2.0 ** -18, np.where(y >= -5, 2.0 ** -17, 2.0 ** -15))
+    got = G.bf16_host(Y[rows])
+    bad = ~(np.abs(got - want) <= (2.0 ** -8 + 1.01 * rel) * np.abs(want) + 2.0 ** -121)
+    assert not bad.any(), (int(bad.sum()), y[bad][:6], got[bad][:6], want[bad][:6])
