@@ -11,7 +11,9 @@
 // What bounds it: shared memory.  A stage is written once and read once by the
 // MMAs, 2 x 248 rows x 128 bytes in the 480 cycles of its MMAs: 132 bytes a
 // cycle of the 128 an SM has, 140 with the epilogue's.  Under load the power
-// cap comes first.
+// cap lowers the clock besides.  (That and whole rounds explain 82 of the 106 us
+// that 4608 x 2560 -> 10240 takes behind its quantizer; the rest is lost per
+// tile, in waits that have not been recorded.)
 //
 // Roles (one CTA per SM, persistent over units of work, 20 warps):
 //   warp 0      producer in both CTAs: per k-stage its halves of the two

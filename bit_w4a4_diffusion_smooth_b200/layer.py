@@ -440,8 +440,9 @@ class FP8Experts(FP8Linear):
     """The FP8 product by expert: rows offsets[e] .. offsets[e+1]-1 of X meet weight e, any share of the rows.
 
     weight: bf16 CUDA [experts, K, N]; bias: bf16 CUDA [experts, N] or None.  `offsets` stay on the device (int32
-    [experts + 1], not decreasing); rows of Y outside every expert's are left as they were (zeros when the call
-    allocates Y).
+    [experts + 1], not decreasing); rows of Y outside every expert's are left as they were.  A call that allocates Y
+    fills it with zeros first, a pass over the whole output: 55 us more on 265 for 9216 rows x 10240, so give a Y
+    where time counts.
     """
 
     def __init__(self, weight, bias=None, epilogue=lib.EPILOGUE_NONE, gelu_col_begin=0):
